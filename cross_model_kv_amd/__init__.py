@@ -5,6 +5,6 @@ include/kvmap.h); ``cross_model_kv_amd.kvmap`` is its ctypes binding.
 """
 
 from . import kvmap  # noqa: F401
-from .kvmap import Context, GramState, KvmapError  # noqa: F401
+from .kvmap import Context, GramState, KvmapError, Q8Cache  # noqa: F401
 
-__all__ = ["kvmap", "Context", "GramState", "KvmapError"]
+__all__ = ["kvmap", "Context", "GramState", "KvmapError", "Q8Cache"]

@@ -168,9 +168,11 @@ struct kvmap_ctx {
     void* static_scratch = nullptr;  // this device's copy of `scratch` (kvmap_gram_noalloc)
     TimingRec timing[kTimingRing];  // events of the last kTimingRing KVMAP_FLAG_TIMING applies
     int64_t n_timed = 0;
+    Q8State q8;                   // the 8-bit cache calls' (q8_api.hip)
 };
 
 int kvmap::context_device(const kvmap_ctx* c) { return c ? c->device : -1; }
+kvmap::Q8State* kvmap::q8_state(kvmap_ctx* c) { return &c->q8; }
 
 // ---------------------------------------------------------------------------------------
 // status / version
@@ -217,6 +219,8 @@ extern "C" int kvmap_create(kvmap_ctx** out, int device) {
     kvmap_ctx* c = new kvmap_ctx();
     c->device = device;
     c->cus = prop.multiProcessorCount;
+    c->q8.device = device;
+    c->q8.cus = prop.multiProcessorCount;
     {
         const int r = resolve_static_scratch(device, &c->static_scratch);
         if (r) {
@@ -231,7 +235,12 @@ extern "C" int kvmap_create(kvmap_ctx** out, int device) {
         kvmap_destroy(c);
         return fail(KVMAP_ERR_OUT_OF_MEMORY, "kvmap_create: hipMalloc failed");
     }
-    if (hipMemcpy(c->d_zero, &zero, sizeof zero, hipMemcpyHostToDevice) != hipSuccess) {
+    if (hipMalloc((void**)&c->q8.dropped, sizeof(unsigned int)) != hipSuccess) {
+        kvmap_destroy(c);
+        return fail(KVMAP_ERR_OUT_OF_MEMORY, "kvmap_create: hipMalloc failed");
+    }
+    if (hipMemcpy(c->d_zero, &zero, sizeof zero, hipMemcpyHostToDevice) != hipSuccess ||
+        hipMemcpy(c->q8.dropped, &zero, sizeof zero, hipMemcpyHostToDevice) != hipSuccess) {
         kvmap_destroy(c);
         return fail(KVMAP_ERR_DEVICE, "kvmap_create: hipMemcpy failed");
     }
@@ -252,6 +261,7 @@ extern "C" int kvmap_destroy(kvmap_ctx* c) {
     }
     (void)hipFree(c->d_count);
     (void)hipFree(c->d_zero);
+    (void)hipFree(c->q8.dropped);
     (void)hipFree(c->ridge);
     if (c->ridge_ov.side) (void)hipStreamDestroy(c->ridge_ov.side);
     if (c->ridge_ov.main_ready) (void)hipEventDestroy(c->ridge_ov.main_ready);

@@ -168,6 +168,44 @@ hipError_t launch_ridge_r2(int n, int p, int q, const RidgeSys* sys, double lamb
 hipError_t launch_fit_select(const double* r2, int L_src, int L_tgt, int H, int k, double* scores,
                              int32_t* sel, hipStream_t s);
 
+// ---- 8-bit paged cache (q8_pages.hip, q8_attend.hip) --------------------------------------
+// Rows of d elements at base + layer/seq/head/token strides (elements).
+struct Q8Rows {
+    void* base;
+    int64_t layer, seq, head, token;
+};
+// The pools of the layers that a call works on: the first layer's, and how far the next one's are.
+struct Q8Pools {
+    uint8_t *k, *v;
+    float *ks, *vs;
+    int64_t layer_codes, layer_scales;  // per layer: n_pages * H * page * d, n_pages * H
+    int n_pages, H, page, d;
+};
+struct Q8Seqs {
+    const int32_t *pages, *start, *count;
+    int B, max_pages;
+};
+hipError_t launch_q8_write(Elem e, const Q8Pools& c, const Q8Seqs& q, int n_layers, int n, const Q8Rows& k,
+                           const Q8Rows& v, unsigned int* dropped, hipStream_t s);
+hipError_t launch_q8_read(Elem e, const Q8Pools& c, const Q8Seqs& q, int n_layers, int n, const Q8Rows& k,
+                          const Q8Rows& v, hipStream_t s);
+struct Q8Attend {
+    Q8Pools c;  // one layer's
+    const int32_t *pages, *len;
+    int B, n_q, Hq, max_pages, max_len;
+    float scale;
+    Q8Rows q, out;
+    float* lse;
+};
+hipError_t launch_q8_attend(Elem e, const Q8Attend& a, hipStream_t s);
+// What a context keeps for these calls.
+struct Q8State {
+    unsigned int* dropped = nullptr;  // pages that writes left out
+    int device = 0;
+    int cus = 0;
+};
+Q8State* q8_state(struct ::kvmap_ctx* c);
+
 // Error reporting shared by the C-ABI files: sets the calling thread's last-error string.
 int report(int status, const char* fmt, ...);
 // HIP device a context is bound to (-1 for NULL).

@@ -1,0 +1,334 @@
+// Writing rows into the 8-bit paged cache and reading them back.
+//
+// One workgroup owns one page of one (layer, sequence, head), keys or values, so the page's scale
+// needs no agreement between workgroups and every element moves once.  For n new rows x of a page
+//   a = max |x| (finite),  e = min { e : a <= 448 * 2^e },  code = rne_e4m3(x * 2^-e),
+// all exact but for that one rounding.  Bytes bound it: es bytes read and one written an element.
+//
+// Thread layout: d / VEC threads side by side on a token's row (16-byte loads), each holding PASSES
+// consecutive tokens, so that a thread has PASSES tokens of VEC dims in registers: a row's codes
+// leave as they are for keys; for values, whose page is dim-major, a thread's PASSES tokens of one dim
+// are adjacent bytes and the page is turned in LDS.
+
+#include "common.h"
+#include "internal.h"
+#include "q8_span.h"
+
+namespace kvmap {
+namespace {
+
+constexpr float kTop = 448.f;  // largest e4m3 value
+constexpr int kMinExp = -110, kMaxExp = 119;
+
+// The smallest power of two 2^e with amax <= 448 * 2^e, e clamped to the scales' range.  With
+// amax = (1 + f) * 2^(x - 1): 448 = 0.875 * 2^9, so e is x - 9, or x - 8 where (1 + f) / 2 > 0.875.
+__device__ __forceinline__ float scale_for(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    int e = (int)(u >> 23) - 126 - 9 + ((u & 0x7FFFFFu) > 0x600000u);
+    e = min(max(e, kMinExp), kMaxExp);
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// Four values to four codes: nearest even, saturating; NaN for what is not finite.
+__device__ __forceinline__ uint32_t codes4(const float* x, float inv) {
+    float y[4];
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[i] = fminf(fmaxf(x[i] * inv, -kTop), kTop);
+        odd |= (__float_as_uint(x[i]) & 0x7F800000u) == 0x7F800000u ? 0xFFu << (8 * i) : 0u;
+    }
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+    return ((uint32_t)w & ~odd) | (0x7F7F7F7Fu & odd);
+}
+
+__device__ __forceinline__ void values4(uint32_t w, float* x) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+    const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    x[0] = a[0];
+    x[1] = a[1];
+    x[2] = b[0];
+    x[3] = b[1];
+}
+
+// Codes of one scale rounded to a larger one (NaN stays NaN).
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+    float x[4];
+    values4(w, x);
+    return codes4(x, ratio);
+}
+
+template <bool BF16>
+struct Row16 {  // 16 bytes of a row as fp32
+    static constexpr int N = BF16 ? 8 : 4;
+    uint4 raw;
+    __device__ __forceinline__ void get(float* x) const {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        if (BF16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = bf16lo(w[i]);
+                x[2 * i + 1] = bf16hi(w[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
+        }
+    }
+    __device__ __forceinline__ void set(const float* x) {
+        if (BF16)
+            raw = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        else
+            raw = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+};
+
+// What one workgroup works on.
+struct Item {
+    int j, b, h, layer, kv;
+};
+__device__ __forceinline__ Item item_of(uint32_t i, int n_slots, int B, int H) {
+    Item t;
+    t.j = (int)(i % n_slots);
+    i /= n_slots;
+    t.h = (int)(i % H);
+    i /= H;
+    t.b = (int)(i % B);
+    i /= B;
+    t.kv = (int)(i & 1);
+    t.layer = (int)(i >> 1);
+    return t;
+}
+
+template <bool BF16, int D, int P>
+struct Tile {
+    static constexpr int ES = BF16 ? 2 : 4;
+    static constexpr int VEC = 16 / ES;
+    static constexpr int TPR = D / VEC;                                // threads on a row
+    static constexpr int PASSES = P * TPR > 256 ? P * TPR / 256 : 1;   // consecutive tokens of a thread
+    static constexpr int LDW = P / 4 + 1;                              // LDS dwords of a dim's tokens (odd: spreads the banks)
+};
+
+template <bool BF16, int D, int P>
+__global__ __launch_bounds__(256) void q8_write_kernel(Q8Pools c, Q8Seqs q, int n_slots, int n, Q8Rows kr, Q8Rows vr,
+                                                       unsigned int* __restrict__ dropped) {
+    using T = Tile<BF16, D, P>;
+    __shared__ uint32_t s_max[4];
+    __shared__ uint32_t turn[D * T::LDW];
+    const Item it = item_of(blockIdx.x, n_slots, q.B, c.H);
+    const int tid = threadIdx.x;
+    const Q8Span sp = q8_span(q.start[it.b], q.count ? q.count[it.b] : n, n, it.j, q.pages + (int64_t)it.b * q.max_pages,
+                              q.max_pages, c.n_pages, P);
+    if (sp.lo >= sp.live) return;
+    if (sp.page < 0) {
+        if (tid == 0 && (!sp.bad_seq || it.j == 0)) atomicAdd(dropped, 1u);
+        return;
+    }
+    const int lo = sp.lo, hi = sp.live;
+
+    const Q8Rows& r = it.kv ? vr : kr;
+    const char* src = (const char*)r.base +
+                      (it.layer * r.layer + it.b * r.seq + it.h * r.head + sp.p0 * r.token) * T::ES;
+    const int row0 = tid / T::TPR * T::PASSES, col = tid % T::TPR * T::VEC;
+    Row16<BF16> x[T::PASSES];
+    uint32_t top = 0;
+#pragma unroll
+    for (int p = 0; p < T::PASSES; ++p) {
+        const int row = row0 + p;
+        x[p].raw = make_uint4(0, 0, 0, 0);
+        if (row >= lo && row < hi) x[p].raw = *(const uint4*)(src + (row * r.token + col) * T::ES);
+        float f[T::VEC];
+        x[p].get(f);
+#pragma unroll
+        for (int i = 0; i < T::VEC; ++i) {
+            const uint32_t u = __float_as_uint(f[i]) & 0x7FFFFFFFu;
+            top = max(top, u < 0x7F800000u ? u : 0u);
+        }
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    if ((tid & 63) == 0) s_max[tid >> 6] = top;
+    __syncthreads();
+    top = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
+
+    const int64_t page = it.layer * c.layer_scales + (int64_t)sp.page * c.H + it.h;
+    float* scale_at = (it.kv ? c.vs : c.ks) + page;
+    uint8_t* dst = (it.kv ? c.v : c.k) + page * (P * D);
+    float scale = scale_for(__uint_as_float(top));
+    if (lo) {
+        const float before = *scale_at;
+        if (before >= scale) {
+            scale = before;
+        } else {  // the tokens before start are rounded to the new scale
+            const float ratio = before / scale;
+            if (it.kv == 0) {
+                for (int i = tid; i < lo * (D / 4); i += 256) {
+                    uint32_t* w = (uint32_t*)dst + i;
+                    *w = rescale4(*w, ratio);
+                }
+            } else {
+                const int wpd = (lo + 3) / 4;  // dwords of a dim that hold such tokens
+                for (int i = tid; i < D * wpd; i += 256) {
+                    const int dim = i / wpd, k = i - dim * wpd;
+                    uint32_t* w = (uint32_t*)(dst + dim * P) + k;
+                    const uint32_t keep = lo - 4 * k >= 4 ? 0u : 0xFFFFFFFFu << (8 * (lo - 4 * k));
+                    *w = (*w & keep) | (rescale4(*w, ratio) & ~keep);
+                }
+            }
+        }
+        __syncthreads();  // `before` is read, and shared dwords of values are written, before the stores below
+    }
+    if (tid == 0) *scale_at = scale;
+    const float inv = 1.f / scale;  // exact: a power of two
+
+    if (it.kv == 0) {
+#pragma unroll
+        for (int p = 0; p < T::PASSES; ++p) {
+            const int row = row0 + p;
+            if (row < lo || row >= hi) continue;
+            float f[T::VEC];
+            x[p].get(f);
+            uint32_t* w = (uint32_t*)(dst + row * D + col);
+            if (BF16)
+                *(uint2*)w = make_uint2(codes4(f, inv), codes4(f + T::VEC - 4, inv));
+            else
+                *w = codes4(f, inv);
+        }
+        return;
+    }
+    // values: PASSES tokens of each of VEC dims
+    uint32_t w[T::PASSES][T::VEC / 4];
+#pragma unroll
+    for (int p = 0; p < T::PASSES; ++p) {
+        float f[T::VEC];
+        x[p].get(f);
+#pragma unroll
+        for (int i = 0; i < T::VEC / 4; ++i) w[p][i] = codes4(f + 4 * i, inv);
+    }
+    if (lo > 0 || hi < P) {  // part of a page: its tokens' bytes alone
+#pragma unroll
+        for (int p = 0; p < T::PASSES; ++p) {
+            const int row = row0 + p;
+            if (row < lo || row >= hi) continue;
+#pragma unroll
+            for (int i = 0; i < T::VEC; ++i) dst[(col + i) * P + row] = (uint8_t)(w[p][i / 4] >> (8 * (i & 3)));
+        }
+        return;
+    }
+    uint8_t* lds = (uint8_t*)turn;
+    if (row0 < P) {
+#pragma unroll
+        for (int i = 0; i < T::VEC; ++i)
+#pragma unroll
+            for (int p = 0; p < T::PASSES; ++p)
+                lds[(col + i) * (T::LDW * 4) + row0 + p] = (uint8_t)(w[p][i / 4] >> (8 * (i & 3)));
+    }
+    __syncthreads();
+    for (int i = tid; i < D * (P / 16); i += 256) {
+        const int dim = i / (P / 16), k = i % (P / 16);
+        const uint32_t* a = turn + dim * T::LDW + 4 * k;
+        *(uint4*)(dst + dim * P + 16 * k) = make_uint4(a[0], a[1], a[2], a[3]);
+    }
+}
+
+template <bool BF16, int D, int P>
+__global__ __launch_bounds__(256) void q8_read_kernel(Q8Pools c, Q8Seqs q, int n_slots, int n, Q8Rows kr, Q8Rows vr) {
+    using T = Tile<BF16, D, P>;
+    __shared__ uint32_t turn[D * T::LDW];
+    const Item it = item_of(blockIdx.x, n_slots, q.B, c.H);
+    const int tid = threadIdx.x;
+    const Q8Span sp = q8_span(q.start[it.b], q.count ? q.count[it.b] : n, n, it.j, q.pages + (int64_t)it.b * q.max_pages,
+                              q.max_pages, c.n_pages, P);
+    if (sp.lo >= sp.hi) return;
+    const bool held = sp.page >= 0;
+    const int lo = sp.lo, hi = sp.hi, live = sp.live;  // rows [live, hi) are zeros
+
+    const Q8Rows& r = it.kv ? vr : kr;
+    char* out = (char*)r.base + (it.layer * r.layer + it.b * r.seq + it.h * r.head + sp.p0 * r.token) * T::ES;
+    const int64_t page = it.layer * c.layer_scales + (int64_t)(held ? sp.page : 0) * c.H + it.h;
+    const uint8_t* src = (it.kv ? c.v : c.k) + page * (P * D);
+    const float scale = held ? (it.kv ? c.vs : c.ks)[page] : __uint_as_float(0x7FC00000u);
+    const int row0 = tid / T::TPR * T::PASSES, col = tid % T::TPR * T::VEC;
+    if (it.kv && held && live > lo) {
+        for (int i = tid; i < D * (P / 16); i += 256) {
+            const int dim = i / (P / 16), k = i % (P / 16);
+            const uint4 a = *(const uint4*)(src + dim * P + 16 * k);
+            uint32_t* w = turn + dim * T::LDW + 4 * k;
+            w[0] = a.x;
+            w[1] = a.y;
+            w[2] = a.z;
+            w[3] = a.w;
+        }
+    }
+    __syncthreads();
+    const uint8_t* lds = (const uint8_t*)turn;
+#pragma unroll
+    for (int p = 0; p < T::PASSES; ++p) {
+        const int row = row0 + p;
+        if (row < lo || row >= hi) continue;
+        float f[T::VEC];
+        if (row >= live) {
+#pragma unroll
+            for (int i = 0; i < T::VEC; ++i) f[i] = 0.f;
+        } else if (!held) {
+#pragma unroll
+            for (int i = 0; i < T::VEC; ++i) f[i] = scale;  // NaN
+        } else {
+#pragma unroll
+            for (int g = 0; g < T::VEC / 4; ++g) {
+                uint32_t w;
+                if (it.kv == 0) {
+                    w = *(const uint32_t*)(src + row * D + col + 4 * g);
+                } else {
+                    const uint8_t* a = lds + (col + 4 * g) * (T::LDW * 4) + row;
+                    w = a[0] | (uint32_t)a[T::LDW * 4] << 8 | (uint32_t)a[2 * T::LDW * 4] << 16 | (uint32_t)a[3 * T::LDW * 4] << 24;
+                }
+                values4(w, f + 4 * g);
+            }
+#pragma unroll
+            for (int i = 0; i < T::VEC; ++i) f[i] *= scale;
+        }
+        Row16<BF16> y;
+        y.set(f);
+        *(uint4*)(out + (row * r.token + col) * T::ES) = y.raw;
+    }
+}
+
+// A row range of n tokens touches at most this many pages.
+int slots(int n, int page) { return (int)(((int64_t)n + 2 * page - 2) / page); }
+
+}  // namespace
+
+#define KVMAP_Q8_PAGES(KERNEL, ...)                                                                         \
+    do {                                                                                                    \
+        const int ns = slots(n, c.page);                                                                    \
+        const dim3 grid((unsigned)((int64_t)ns * q.B * c.H * n_layers * 2));                                \
+        if (e == Elem::BF16) {                                                                              \
+            if (c.d == 128) KVMAP_Q8_P(KERNEL, true, 128, __VA_ARGS__); else KVMAP_Q8_P(KERNEL, true, 64, __VA_ARGS__); \
+        } else {                                                                                            \
+            if (c.d == 128) KVMAP_Q8_P(KERNEL, false, 128, __VA_ARGS__); else KVMAP_Q8_P(KERNEL, false, 64, __VA_ARGS__); \
+        }                                                                                                   \
+    } while (0)
+#define KVMAP_Q8_P(KERNEL, B, D, ...)                                                                           \
+    do {                                                                                                        \
+        if (c.page == 16) hipLaunchKernelGGL((KERNEL<B, D, 16>), grid, dim3(256), 0, s, c, q, ns, n, __VA_ARGS__);       \
+        else if (c.page == 32) hipLaunchKernelGGL((KERNEL<B, D, 32>), grid, dim3(256), 0, s, c, q, ns, n, __VA_ARGS__);  \
+        else if (c.page == 64) hipLaunchKernelGGL((KERNEL<B, D, 64>), grid, dim3(256), 0, s, c, q, ns, n, __VA_ARGS__);  \
+        else hipLaunchKernelGGL((KERNEL<B, D, 128>), grid, dim3(256), 0, s, c, q, ns, n, __VA_ARGS__);                   \
+    } while (0)
+
+hipError_t launch_q8_write(Elem e, const Q8Pools& c, const Q8Seqs& q, int n_layers, int n, const Q8Rows& k,
+                           const Q8Rows& v, unsigned int* dropped, hipStream_t s) {
+    KVMAP_Q8_PAGES(q8_write_kernel, k, v, dropped);
+    return hipGetLastError();
+}
+
+hipError_t launch_q8_read(Elem e, const Q8Pools& c, const Q8Seqs& q, int n_layers, int n, const Q8Rows& k,
+                          const Q8Rows& v, hipStream_t s) {
+    KVMAP_Q8_PAGES(q8_read_kernel, k, v);
+    return hipGetLastError();
+}
+
+}  // namespace kvmap

@@ -1,0 +1,47 @@
+// Which rows of which page a workgroup of the 8-bit cache's calls works on.  Plain integer code
+// without HIP headers, so that the same functions run in the kernels and in a host build of the tests.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __HIPCC__
+#define KVMAP_HD __host__ __device__ __forceinline__
+#else
+#define KVMAP_HD inline
+#endif
+
+namespace kvmap {
+
+// The page of a sequence's slot, or -1 where the table has none that lies in the pool.
+KVMAP_HD int q8_page_at(const int32_t* table, int64_t slot, int max_pages, int n_pages) {
+    if (slot < 0 || slot >= max_pages) return -1;
+    const int32_t p = table[slot];
+    return p >= 0 && p < n_pages ? p : -1;
+}
+
+// Rows [lo, hi) of one page are the tokens p0 + lo .. p0 + hi of a sequence that a call covers; of them the
+// rows below `live` belong to the sequence's own count.
+struct Q8Span {
+    int64_t p0;      // position of the page's row 0, less the sequence's start
+    int lo, hi, live;
+    int page;        // -1: out of range
+    bool bad_seq;    // start or count out of range: nothing of the sequence is held
+};
+
+// The j-th page that tokens start .. start + n can touch; lo >= hi where they do not reach it.
+KVMAP_HD Q8Span q8_span(int64_t start, int64_t count, int64_t n, int64_t j, const int32_t* table, int max_pages,
+                        int n_pages, int P) {
+    Q8Span s;
+    s.bad_seq = start < 0 || count < 0 || count > n;
+    if (s.bad_seq) start = 0, count = n;
+    const int64_t slot = start / P + j, at = slot * P;
+    s.p0 = at - start;
+    const int64_t lo = start - at, hi = start + n - at, live = start + count - at;
+    s.lo = (int)(lo > 0 ? lo : 0);
+    s.hi = (int)(hi < P ? (hi > 0 ? hi : 0) : P);
+    s.live = (int)(live < s.hi ? (live > 0 ? live : 0) : s.hi);
+    s.page = !s.bad_seq && s.lo < s.live ? q8_page_at(table, slot, max_pages, n_pages) : -1;
+    return s;
+}
+
+}  // namespace kvmap

@@ -83,6 +83,22 @@ class FitPassC(ctypes.Structure):
                 ("pass_", ctypes.c_int32), ("passes", ctypes.c_int32)]
 
 
+class Q8CacheC(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class Q8SeqsC(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("pages", ctypes.c_void_p),
+                ("start", ctypes.c_void_p), ("count", ctypes.c_void_p)]
+
+
+class Q8RowsC(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("layer_stride", ctypes.c_int64), ("seq_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 _SIGS = {
@@ -136,7 +152,22 @@ _SIGS = {
     "kvmap_fit_add": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p]),
     "kvmap_fit_destroy": (ctypes.c_int, [ctypes.c_void_p]),
+    "kvmap_q8_dropped": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32), ctypes.c_void_p]),
+    "kvmap_q8_reserve": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(Q8CacheC), ctypes.c_int32, ctypes.c_int32,
+                                        ctypes.c_int32, ctypes.c_int32]),
 }
+_Q8_ROWS = [ctypes.POINTER(Q8CacheC), ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(Q8SeqsC), ctypes.c_int32,
+            ctypes.c_int32, ctypes.POINTER(Q8RowsC), ctypes.POINTER(Q8RowsC)]
+_Q8_ATTEND = [ctypes.POINTER(Q8CacheC), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+              ctypes.POINTER(Q8RowsC), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+              ctypes.c_double, ctypes.POINTER(Q8RowsC), ctypes.c_void_p]
+_SIGS.update({
+    "kvmap_q8_write": (ctypes.c_int, [ctypes.c_void_p] + _Q8_ROWS + [ctypes.c_void_p]),
+    "kvmap_q8_read": (ctypes.c_int, [ctypes.c_void_p] + _Q8_ROWS + [ctypes.c_void_p]),
+    "kvmap_q8_attend": (ctypes.c_int, [ctypes.c_void_p] + _Q8_ATTEND + [ctypes.c_void_p]),
+    "kvmap_validate_q8_rows": (ctypes.c_int, _Q8_ROWS + [ctypes.c_int32]),
+    "kvmap_validate_q8_attend": (ctypes.c_int, _Q8_ATTEND),
+})
 
 
 def lib():
@@ -211,6 +242,23 @@ def validate_gram(p, q, n, mean_x, mean_y, M_xx, M_xy, ss_y, xx_block, X, Y, n_b
     st = GramStateC(int(n), int(p), int(q), mean_x or None, mean_y or None, M_xx or None, M_xy or None,
                     ss_y or None, int(xx_block))
     return lib().kvmap_validate_gram(ctypes.byref(st), X or None, Y or None, int(n_b), int(dtype))
+
+
+def validate_q8_rows(cache: Q8CacheC, layer0, n_layers, seqs: Q8SeqsC, n, dtype, k: Q8RowsC, v: Q8RowsC,
+                     output: bool = False) -> int:
+    """kvmap_validate_q8_rows on structs of addresses (nothing is read; None passes NULL); returns the
+    status code (host only, needs no GPU)."""
+    ref = lambda x: None if x is None else ctypes.byref(x)
+    return lib().kvmap_validate_q8_rows(ref(cache), layer0, n_layers, ref(seqs), n, dtype, ref(k), ref(v), int(output))
+
+
+def validate_q8_attend(cache: Q8CacheC, layer, B, n_q, H_q, dtype, q: Q8RowsC, pages, max_pages, lens, max_len,
+                       scale, out: Q8RowsC, lse=None) -> int:
+    """kvmap_validate_q8_attend on structs and addresses (nothing is read; None passes NULL); returns the
+    status code (host only, needs no GPU)."""
+    ref = lambda x: None if x is None else ctypes.byref(x)
+    return lib().kvmap_validate_q8_attend(ref(cache), layer, B, n_q, H_q, dtype, ref(q), pages, max_pages, lens,
+                                          max_len, scale, ref(out), lse)
 
 
 def ridge_solve_host(mean_x, mean_y, M_xx, M_xy, lam: float, n_threads: int = 0):
@@ -290,6 +338,33 @@ class GramState:
     @property
     def n(self) -> int:
         return int(self.c.n)
+
+
+class Q8Cache:
+    """A cache in 8 bits (kvmap_q8_cache) over the caller's device tensors:
+    k [L][n_pages][H][page][d] and v [L][n_pages][H][d][page] torch.float8_e4m3fn, k_scale and v_scale
+    [L][n_pages][H] float32.  Context.q8_cache allocates one."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
+        if k.dim() != 5:
+            raise ValueError("k must be [L][n_pages][H][page][d]")
+        L, n_pages, H, page, d = (int(x) for x in k.shape)
+        if tuple(v.shape) != (L, n_pages, H, d, page):
+            raise ValueError("v must be [L][n_pages][H][d][page], a page of values being dim-major")
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype != torch.float8_e4m3fn:
+                raise TypeError(f"{name} must be torch.float8_e4m3fn")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if tuple(t.shape) != (L, n_pages, H) or t.dtype != torch.float32:
+                raise ValueError(f"{name} must be float32 [L][n_pages][H]")
+        if not k.device == v.device == k_scale.device == v_scale.device:
+            raise ValueError("the cache's tensors must be on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.L, self.n_pages, self.H, self.page, self.d = L, n_pages, H, page, d
+        self.c = Q8CacheC(L, n_pages, H, page, d, _dev_ptr(k, "k"), _dev_ptr(v, "v"), _dev_ptr(k_scale, "k_scale"),
+                          _dev_ptr(v_scale, "v_scale"))
+        self.ref = ctypes.byref(self.c)
 
 
 class Context:
@@ -400,6 +475,120 @@ class Context:
                                   ctypes.byref(rs), ctypes.byref(rt), _stream_handle(stream, src.device)),
                "kvmap_recode")
         return out
+
+    # ---- 8-bit paged cache -------------------------------------------------------------
+    def q8_cache(self, L: int, n_pages: int, H: int, page: int, d: int) -> Q8Cache:
+        """An empty Q8Cache on the context's device."""
+        torch = _torch()
+        dev = torch.device("cuda", self.device)
+        codes = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+        scales = lambda: torch.zeros((L, n_pages, H), dtype=torch.float32, device=dev)
+        return Q8Cache(codes(L, n_pages, H, page, d), codes(L, n_pages, H, d, page), scales(), scales())
+
+    def _q8_ints(self, t, name, shape):
+        torch = _torch()
+        if t.dtype != torch.int32 or t.shape != shape:
+            raise ValueError(f"{name} must be int32 {list(shape)}")
+        return _dev_ptr(t, name)
+
+    def _q8_rows(self, name, cache, k, v, pages, start, n, count, layer, dtype, stream):
+        B, max_pages = pages.shape
+        L = k.shape[0]
+        shape = (L, B, cache.H, n, cache.d)
+        if k.shape != shape or v.shape != shape:
+            raise ValueError(f"k and v must be {list(shape)} ([layers][B][H][n][d], or [B][H][n][d] of one layer)")
+        if not (k.is_cuda and v.is_cuda):
+            raise ValueError("k and v must be device tensors")
+        ks, vs = k.stride(), v.stride()
+        if ks[4] != 1 or vs[4] != 1:
+            raise ValueError("the head dim of k and v must be contiguous")
+        seqs = Q8SeqsC(B, max_pages, self._q8_ints(pages, "pages", (B, max_pages)), self._q8_ints(start, "start", (B,)),
+                       None if count is None else self._q8_ints(count, "count", (B,)))
+        st = getattr(lib(), name)(self._h, cache.ref, layer, L, ctypes.byref(seqs), n, dtype,
+                                  ctypes.byref(Q8RowsC(k.data_ptr(), ks[0], ks[1], ks[2], ks[3])),
+                                  ctypes.byref(Q8RowsC(v.data_ptr(), vs[0], vs[1], vs[2], vs[3])),
+                                  _stream_handle(stream, cache.k.device))
+        if st:
+            _check(st, name)
+
+    def q8_write(self, cache: Q8Cache, k, v, pages, start, count=None, layer: int = 0, stream=None):
+        """kvmap_q8_write: rows k, v [layers][B][H][n][d] (or [B][H][n][d] of one layer; device, bf16 or fp32, any
+        strides of whole 16 bytes over a contiguous head dim) enter layers layer .. of the cache as tokens
+        start[b] .. start[b] + count[b] (n each without count) of the sequences whose pages are listed in
+        pages [B][max_pages].  pages, start and count: device int32."""
+        if k.dim() == 4:
+            k, v = k.unsqueeze(0), v.unsqueeze(0)
+        if k.dim() != 5:
+            raise ValueError("k and v must be [layers][B][H][n][d] or [B][H][n][d]")
+        if k.dtype != v.dtype:
+            raise TypeError(f"v dtype {v.dtype} differs from k {k.dtype}")
+        self._q8_rows("kvmap_q8_write", cache, k, v, pages, start, k.shape[3], count, layer, _dtype_code(k), stream)
+
+    def q8_read(self, cache: Q8Cache, pages, start, n: int, count=None, layer: int = 0, n_layers: int | None = None,
+                dtype=None, out_k=None, out_v=None, stream=None):
+        """kvmap_q8_read: (k, v) [n_layers][B][H][n][d], the n tokens from start[b] of every sequence, zeros past
+        count[b].  n_layers defaults to the layers from `layer` on; dtype (bf16 by default) to out_k's."""
+        torch = _torch()
+        L = cache.L - layer if n_layers is None else n_layers
+        if dtype is None:
+            dtype = out_k.dtype if out_k is not None else torch.bfloat16
+        shape = (L, pages.shape[0], cache.H, n, cache.d)
+        if out_k is None:
+            out_k = torch.empty(shape, dtype=dtype, device=cache.k.device)
+        if out_v is None:
+            out_v = torch.empty(shape, dtype=dtype, device=cache.k.device)
+        if out_k.dtype != dtype or out_v.dtype != dtype:
+            raise TypeError("out_k and out_v must be of the dtype asked for")
+        self._q8_rows("kvmap_q8_read", cache, out_k, out_v, pages, start, n, count, layer, _dtype_code(out_k), stream)
+        return out_k, out_v
+
+    def q8_dropped(self, stream=None) -> int:
+        """kvmap_q8_dropped: pages that writes left out since the last call (synchronises)."""
+        n = ctypes.c_uint32()
+        _check(lib().kvmap_q8_dropped(self._h, ctypes.byref(n), _stream_handle(stream, self.device)), "kvmap_q8_dropped")
+        return int(n.value)
+
+    def q8_reserve(self, cache: Q8Cache, B: int, n_q: int, H_q: int, max_len: int):
+        """kvmap_q8_reserve: size the scratch for q8_attend calls up to these sizes."""
+        _check(lib().kvmap_q8_reserve(self._h, cache.ref, B, n_q, H_q, max_len), "kvmap_q8_reserve")
+
+    def q8_attend(self, cache: Q8Cache, q, pages, lens, max_len: int, layer: int = 0, scale: float | None = None,
+                  out=None, lse=None, stream=None):
+        """kvmap_q8_attend: attention of the last n_q tokens of every sequence, q [B][n_q][H_q][d] (device, bf16 or
+        fp32, any strides of whole 16 bytes over a contiguous head dim), over layer `layer` of the cache.  pages
+        [B][max_pages] and lens [B] are device int32; max_len (host) bounds the lengths; scale defaults to
+        d^-1/2.  Returns out (allocated if not given), or (out, lse) where lse is a float32 [B][n_q][H_q]
+        tensor or True."""
+        torch = _torch()
+        if q.dim() != 4 or q.shape[3] != cache.d:
+            raise ValueError(f"q must be [B][n_q][H_q][{cache.d}]")
+        B, n_q, H_q, d = q.shape
+        max_pages = pages.shape[-1]
+        if out is None:
+            out = torch.empty((B, n_q, H_q, d), dtype=q.dtype, device=q.device)
+        if out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must match q's shape and dtype")
+        if not (q.is_cuda and out.is_cuda):
+            raise ValueError("q and out must be device tensors")
+        qs, os_ = q.stride(), out.stride()
+        if qs[3] != 1 or os_[3] != 1:
+            raise ValueError("the head dim of q and out must be contiguous")
+        lse_ptr = None
+        if lse is not None and lse is not False:
+            if lse is True:
+                lse = torch.empty((B, n_q, H_q), dtype=torch.float32, device=q.device)
+            elif lse.shape != (B, n_q, H_q) or lse.dtype != torch.float32:
+                raise ValueError("lse must be float32 [B][n_q][H_q]")
+            lse_ptr = _dev_ptr(lse, "lse")
+        st = lib().kvmap_q8_attend(self._h, cache.ref, layer, B, n_q, H_q, _dtype_code(q),
+                                   ctypes.byref(Q8RowsC(q.data_ptr(), 0, qs[0], qs[2], qs[1])),
+                                   self._q8_ints(pages, "pages", (B, max_pages)), max_pages,
+                                   self._q8_ints(lens, "lens", (B,)), max_len, d ** -0.5 if scale is None else scale,
+                                   ctypes.byref(Q8RowsC(out.data_ptr(), 0, os_[0], os_[2], os_[1])), lse_ptr,
+                                   _stream_handle(stream, q.device))
+        if st:
+            _check(st, "kvmap_q8_attend")
+        return out if lse_ptr is None else (out, lse)
 
     # ---- fit-side statistics ---------------------------------------------------------
     def cache_rows(self, cache, layers, theta: float | None = None, pos0: int = 0, out=None, stream=None,

@@ -477,6 +477,116 @@ int kvmap_fit_add(kvmap_fit* fit, const void* src_k, const void* src_v, const vo
 /* Free the fit's device memory (synchronises the device). NULL is a no-op. */
 int kvmap_fit_destroy(kvmap_fit* fit);
 
+/* ---- 8-bit paged cache ------------------------------------------------------------- */
+
+/* A cache held in 8 bits for decoding on it: pages of `page` tokens, e4m3 codes (the OCP form: sign,
+ * 4 exponent and 3 mantissa bits, largest value 448, no infinities) and one scale for each (layer, page,
+ * KV head), keys and values apart; a stored value is scale * code.
+ *   k        device [L][n_pages][H_kv][page][head_dim]   codes of the keys
+ *   v        device [L][n_pages][H_kv][head_dim][page]   codes of the values: a page is held dim-major,
+ *                                                        because attention sums values over tokens
+ *   k_scale, v_scale  device fp32 [L][n_pages][H_kv]     powers of two 2^e, -110 <= e <= 119
+ * Scales are powers of two so that no step but the rounding to a code loses anything: x / scale is exact
+ * in fp32, scale * code is exact in bf16, and a page whose scale grows moves its codes by whole exponents.
+ * (e4m3 is a floating format: a scale up to twice as large as need be costs it no precision in the
+ * normal range.)
+ * All buffers are the caller's, 16-byte aligned; the struct only points at them. */
+typedef struct {
+    int32_t L, n_pages, H_kv, page, head_dim; /* page: 16, 32, 64 or 128; head_dim: 64 or 128 */
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+} kvmap_q8_cache;
+
+/* The sequences of a call.  Token t of sequence b lives in page pages[b * max_pages + t / page], row
+ * t % page.  Entries past a sequence's last token are not read.  No page may belong to two sequences
+ * of one write. */
+typedef struct {
+    int32_t B, max_pages;
+    const int32_t* pages; /* device [B][max_pages]                                       */
+    const int32_t* start; /* device [B]: position of the call's first token of sequence b */
+    const int32_t* count; /* device [B]: its tokens in this call, 0 .. n; NULL: n each    */
+} kvmap_q8_seqs;
+
+/* Rows of head_dim elements anywhere in device memory: the row of (layer, sequence, head, token) starts
+ * at element layer * layer_stride + seq * seq_stride + head * head_stride + token * token_stride.
+ * The base is 16-byte aligned, and so is every stride in bytes; strides are >= 0, and those of an output
+ * leave no two rows overlapping. */
+typedef struct {
+    void* base;
+    int64_t layer_stride, seq_stride, head_stride, token_stride; /* in elements */
+} kvmap_q8_rows;
+
+/* Write tokens start[b] .. start[b] + count[b] of every sequence into layers layer0 .. layer0 + n_layers of
+ * the cache, rounding them to 8 bits.  k, v: rows (layer - layer0, b, head, i), i < count[b], in `dtype`; a
+ * mapped cache [L][H][T][d] of kvmap_apply and the key and value parts of one projection's output
+ * [B][n][parts][d] are both such rows.  For every page that tokens enter, and every head, keys and values
+ * each on their own:
+ *   a     = the largest finite |x| entering;  e = the smallest exponent with a <= 448 * 2^e, in [-110, 119]
+ *   scale = 2^e, or the page's scale so far if that is larger and the page holds tokens before start[b]
+ *   code  = x / scale rounded to nearest even (saturating at 448; NaN for a NaN or an infinity, which stays
+ *           visible that way and leaves the page's scale alone)
+ *   codes of the tokens before start[b] are rounded to the new scale when it grew
+ * Codes past the sequence's new end are left as they are.  What a write stores does not depend on what
+ * other sequences do; writing the same tokens again changes nothing.
+ * A token whose position or page is out of range (start < 0, count outside 0 .. n, beyond max_pages, a page
+ * outside 0 .. n_pages - 1) is not written, and counted: see kvmap_q8_dropped.
+ * Asynchronous on `stream`, allocates nothing, may be captured into a graph.
+ * Errors (nothing written): INVALID_ARGUMENT (NULL, alignment, strides, overlapping buffers), SHAPE (sizes,
+ * layer range), UNSUPPORTED (dtype, head_dim, page). */
+int kvmap_q8_write(kvmap_ctx* ctx, const kvmap_q8_cache* cache, int32_t layer0, int32_t n_layers,
+                   const kvmap_q8_seqs* seqs, int32_t n, int32_t dtype, const kvmap_q8_rows* k,
+                   const kvmap_q8_rows* v, void* stream);
+/* Read the same tokens back: k, v rows (layer - layer0, b, head, i) get scale * code, rounded to `dtype` (exact
+ * in bf16 and fp32), zeros for count[b] <= i < n, and NaN where the position or the page is out of range.
+ * Asynchronous on `stream`, allocates nothing, may be captured.  Errors as kvmap_q8_write. */
+int kvmap_q8_read(kvmap_ctx* ctx, const kvmap_q8_cache* cache, int32_t layer0, int32_t n_layers,
+                  const kvmap_q8_seqs* seqs, int32_t n, int32_t dtype, const kvmap_q8_rows* k,
+                  const kvmap_q8_rows* v, void* stream);
+/* Pages (of one layer, head, and keys or values) that writes on this context have left out since the last
+ * call because a position or page was out of range; *n gets the count, which starts again at 0.
+ * Synchronises `stream`. */
+int kvmap_q8_dropped(kvmap_ctx* ctx, uint32_t* n, void* stream);
+
+/* Attention of the last n_q tokens of every sequence over one layer of the cache:
+ *   y(b, i, h, t) = scale * q(b, i, h) . key(t),  t <= len[b] - n_q + i, key and value head h / (H_q / H_kv)
+ *   lse = log sum_t exp y,   out = sum_t exp(y - lse) value(t)
+ * The queries' own keys and values have been written before.  A row that sees no token (len[b] = 0, or row
+ * i < n_q - len[b]) gives out = 0 and lse = -infinity.  Tokens that a row does not see do not touch it,
+ * whatever they hold.
+ *   q, out   rows (0, b, query head, i) in `dtype` (layer_stride is not used);  H_q a multiple of H_kv
+ *   pages, max_pages  as in kvmap_q8_seqs;  len  device int32 [B]
+ *   max_len  host: no len[b] is larger (it sizes the launch, so that lengths may grow between replays of a
+ *            captured graph)
+ *   lse      device fp32 [B][n_q][H_q], natural logarithm, or NULL
+ * A sequence whose len is out of range (negative, above max_len or max_pages * page) gives NaN, and so does a
+ * row that sees a token of a page outside 0 .. n_pages - 1.
+ * bf16: products with bf16 queries and fp16 softmax weights on the matrix cores (11 bits, so that the output's
+ * own rounding is what counts), sums and statistics in fp32.  fp32: queries as three bf16 parts, weights as two
+ * fp16 parts, so that products keep the 24 and 22 bits.
+ * Repeated calls give identical outputs.  Asynchronous on `stream`.  Long caches are split over workgroups
+ * whose results are joined through a scratch buffer that the context owns: it grows on first use
+ * (kvmap_q8_reserve sizes it ahead), and a buffer outgrown is kept until kvmap_destroy, since a captured graph
+ * may still use it.  A call that would have to grow it while `stream` is being captured is refused
+ * (INVALID_ARGUMENT).  Errors as kvmap_q8_write. */
+int kvmap_q8_attend(kvmap_ctx* ctx, const kvmap_q8_cache* cache, int32_t layer, int32_t B, int32_t n_q, int32_t H_q,
+                    int32_t dtype, const kvmap_q8_rows* q, const int32_t* pages, int32_t max_pages,
+                    const int32_t* len, int32_t max_len, double scale, const kvmap_q8_rows* out, float* lse,
+                    void* stream);
+/* Size the scratch for kvmap_q8_attend calls of this cache, B, n_q, H_q and max_len, or smaller ones.  Refused
+ * as kvmap_q8_attend refuses the sizes.  Synchronous. */
+int kvmap_q8_reserve(kvmap_ctx* ctx, const kvmap_q8_cache* cache, int32_t B, int32_t n_q, int32_t H_q,
+                     int32_t max_len);
+/* Host-only checks of the calls above, run by them before any device work (buffers are taken as addresses,
+ * nothing is read).  `output` != 0: the rows are written (kvmap_q8_read).  Need no device. */
+int kvmap_validate_q8_rows(const kvmap_q8_cache* cache, int32_t layer0, int32_t n_layers, const kvmap_q8_seqs* seqs,
+                           int32_t n, int32_t dtype, const kvmap_q8_rows* k, const kvmap_q8_rows* v, int32_t output);
+int kvmap_validate_q8_attend(const kvmap_q8_cache* cache, int32_t layer, int32_t B, int32_t n_q, int32_t H_q,
+                             int32_t dtype, const kvmap_q8_rows* q, const int32_t* pages, int32_t max_pages,
+                             const int32_t* len, int32_t max_len, double scale, const kvmap_q8_rows* out,
+                             const float* lse);
+
 #ifdef __cplusplus
 }
 #endif
