@@ -262,6 +262,7 @@ extern "C" int kvmap_destroy(kvmap_ctx* c) {
     (void)hipFree(c->d_count);
     (void)hipFree(c->d_zero);
     (void)hipFree(c->q8.dropped);
+    (void)hipFree(c->q8.scratch);
     (void)hipFree(c->ridge);
     if (c->ridge_ov.side) (void)hipStreamDestroy(c->ridge_ov.side);
     if (c->ridge_ov.main_ready) (void)hipEventDestroy(c->ridge_ov.main_ready);

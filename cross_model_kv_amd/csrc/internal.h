@@ -197,10 +197,18 @@ struct Q8Attend {
     Q8Rows q, out;
     float* lse;
 };
-hipError_t launch_q8_attend(Elem e, const Q8Attend& a, hipStream_t s);
+// The launch of one attention call: fixed by the host's sizes alone.
+struct Q8Plan {
+    int nt, row_blocks;   // 16-row tiles of a workgroup, workgroups over a sequence's rows
+    int n_splits, tps;    // workgroups over its tokens, 64-token tiles of each
+};
+size_t q8_scratch_bytes(int cus);  // enough for every plan
+Q8Plan q8_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus);
+hipError_t launch_q8_attend(Elem e, const Q8Attend& a, const Q8Plan& p, void* scratch, hipStream_t s);
 // What a context keeps for these calls.
 struct Q8State {
     unsigned int* dropped = nullptr;  // pages that writes left out
+    void* scratch = nullptr;          // attention's partial results
     int device = 0;
     int cus = 0;
 };

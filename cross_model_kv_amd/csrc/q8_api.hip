@@ -161,7 +161,7 @@ extern "C" int kvmap_validate_q8_rows(const kvmap_q8_cache* c, int32_t layer0, i
     if (n < 1 || n > (1 << 30)) return report(KVMAP_ERR_SHAPE, "n must be in [1, 2^30]");
     // one workgroup for each page that n tokens can touch, sequence, head, layer, and keys or values
     const double items = (double)((n + 2 * (int64_t)c->page - 2) / c->page) * q->B * c->H_kv * n_layers * 2.0;
-    if (items >= 2147483648.0) return report(KVMAP_ERR_SHAPE, "the call covers too many pages (%.0f): split it", items);
+    if (items >= 16777216.0) return report(KVMAP_ERR_SHAPE, "the call covers too many pages (%.0f): split it", items);
     Range r[8];
     cache_ranges(c, r);
     st = check_disjoint(c);
@@ -242,8 +242,8 @@ static int check_attend_sizes(const kvmap_q8_cache* c, int32_t B, int32_t n_q, i
     if (B < 1 || n_q < 1) return report(KVMAP_ERR_SHAPE, "B and n_q must be >= 1");
     if (H_q < 1 || H_q % c->H_kv) return report(KVMAP_ERR_SHAPE, "H_q = %d is not a multiple of H_kv = %d", (int)H_q, (int)c->H_kv);
     if (max_len < 0 || max_len >= (1 << 30)) return report(KVMAP_ERR_SHAPE, "max_len must be in [0, 2^30)");
-    if ((int64_t)B * c->H_kv > 65535 || (double)n_q * H_q >= 1073741824.0 || (double)B * n_q * H_q >= 2147483648.0)
-        return report(KVMAP_ERR_SHAPE, "B * H_kv must stay below 2^16, n_q * H_q below 2^30 and B * n_q * H_q below 2^31");
+    if ((int64_t)B * c->H_kv > 65535 || (double)n_q * H_q >= 268435456.0 || (double)B * n_q * H_q >= 2147483648.0)
+        return report(KVMAP_ERR_SHAPE, "B * H_kv must stay below 2^16, n_q * H_q below 2^28 and B * n_q * H_q below 2^31");
     return KVMAP_OK;
 }
 
@@ -286,11 +286,31 @@ extern "C" int kvmap_validate_q8_attend(const kvmap_q8_cache* c, int32_t layer, 
     return KVMAP_OK;
 }
 
+// Attention's scratch, of one size for every call: allocated once, so its address never changes under a
+// captured graph.
+static int ensure_scratch(Q8State* s, hipStream_t stream, bool in_call) {
+    if (s->scratch) return KVMAP_OK;
+    if (in_call) {
+        hipStreamCaptureStatus capturing = hipStreamCaptureStatusNone;
+        Q8_HIP(hipStreamIsCapturing(stream, &capturing));
+        if (capturing != hipStreamCaptureStatusNone)
+            return report(KVMAP_ERR_INVALID_ARGUMENT, "kvmap_q8_attend: the stream is being captured and the context has no scratch "
+                          "yet; call kvmap_q8_reserve first");
+    }
+    Q8_HIP(hipMalloc(&s->scratch, q8_scratch_bytes(s->cus)));
+    return KVMAP_OK;
+}
+
 extern "C" int kvmap_q8_reserve(kvmap_ctx* ctx, const kvmap_q8_cache* c, int32_t B, int32_t n_q, int32_t H_q,
                                 int32_t max_len) {
     const int st = check_attend_sizes(c, B, n_q, H_q, max_len);
     if (st) return st;
     if (!ctx) return report(KVMAP_ERR_INVALID_ARGUMENT, "kvmap_q8_reserve: ctx is NULL");
+    Q8State* s = q8_state(ctx);
+    OnDevice on(s->device);
+    if (!on.okay) return report(KVMAP_ERR_DEVICE, "kvmap_q8_reserve: hipSetDevice(%d) failed", s->device);
+    const int r = ensure_scratch(s, nullptr, false);
+    if (r) return r;
     report(KVMAP_OK, "%s", "");
     return KVMAP_OK;
 }
@@ -306,6 +326,11 @@ extern "C" int kvmap_q8_attend(kvmap_ctx* ctx, const kvmap_q8_cache* c, int32_t 
     OnDevice on(s->device);
     if (!on.okay) return report(KVMAP_ERR_DEVICE, "kvmap_q8_attend: hipSetDevice(%d) failed", s->device);
     Q8Attend a{pools(c, layer), pages, len, B, n_q, H_q, max_pages, max_len, (float)scale, rows(q), rows(out), lse};
-    Q8_HIP(launch_q8_attend(dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32, a, (hipStream_t)stream));
+    const Q8Plan plan = q8_attend_plan(dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32, B, n_q, H_q, c->H_kv, c->head_dim, max_len, s->cus);
+    if (plan.n_splits > 1) {
+        const int r = ensure_scratch(s, (hipStream_t)stream, true);
+        if (r) return r;
+    }
+    Q8_HIP(launch_q8_attend(dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32, a, plan, s->scratch, (hipStream_t)stream));
     return KVMAP_OK;
 }

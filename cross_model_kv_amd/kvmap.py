@@ -549,7 +549,7 @@ class Context:
         return int(n.value)
 
     def q8_reserve(self, cache: Q8Cache, B: int, n_q: int, H_q: int, max_len: int):
-        """kvmap_q8_reserve: size the scratch for q8_attend calls up to these sizes."""
+        """kvmap_q8_reserve: allocate the scratch of q8_attend calls of these sizes ahead (before a capture)."""
         _check(lib().kvmap_q8_reserve(self._h, cache.ref, B, n_q, H_q, max_len), "kvmap_q8_reserve")
 
     def q8_attend(self, cache: Q8Cache, q, pages, lens, max_len: int, layer: int = 0, scale: float | None = None,

@@ -563,19 +563,18 @@ int kvmap_q8_dropped(kvmap_ctx* ctx, uint32_t* n, void* stream);
  * A sequence whose len is out of range (negative, above max_len or max_pages * page) gives NaN, and so does a
  * row that sees a token of a page outside 0 .. n_pages - 1.
  * bf16: products with bf16 queries and fp16 softmax weights on the matrix cores (11 bits, so that the output's
- * own rounding is what counts), sums and statistics in fp32.  fp32: queries as three bf16 parts, weights as two
- * fp16 parts, so that products keep the 24 and 22 bits.
+ * own rounding is what counts), sums and statistics in fp32.  fp32: queries and weights as three bf16 parts each,
+ * so that products keep 24 bits.
  * Repeated calls give identical outputs.  Asynchronous on `stream`.  Long caches are split over workgroups
- * whose results are joined through a scratch buffer that the context owns: it grows on first use
- * (kvmap_q8_reserve sizes it ahead), and a buffer outgrown is kept until kvmap_destroy, since a captured graph
- * may still use it.  A call that would have to grow it while `stream` is being captured is refused
- * (INVALID_ARGUMENT).  Errors as kvmap_q8_write. */
+ * whose results are joined through a scratch buffer that the context owns: of one size for all calls, allocated
+ * by kvmap_q8_reserve or by the first call that needs it, and kept until kvmap_destroy.  A call that would have to
+ * allocate it while `stream` is being captured is refused (INVALID_ARGUMENT).  Errors as kvmap_q8_write. */
 int kvmap_q8_attend(kvmap_ctx* ctx, const kvmap_q8_cache* cache, int32_t layer, int32_t B, int32_t n_q, int32_t H_q,
                     int32_t dtype, const kvmap_q8_rows* q, const int32_t* pages, int32_t max_pages,
                     const int32_t* len, int32_t max_len, double scale, const kvmap_q8_rows* out, float* lse,
                     void* stream);
-/* Size the scratch for kvmap_q8_attend calls of this cache, B, n_q, H_q and max_len, or smaller ones.  Refused
- * as kvmap_q8_attend refuses the sizes.  Synchronous. */
+/* Prepare for kvmap_q8_attend calls of this cache, B, n_q, H_q and max_len: allocates the scratch where there is
+ * none yet.  Refused as kvmap_q8_attend refuses the sizes.  Synchronous. */
 int kvmap_q8_reserve(kvmap_ctx* ctx, const kvmap_q8_cache* cache, int32_t B, int32_t n_q, int32_t H_q,
                      int32_t max_len);
 /* Host-only checks of the calls above, run by them before any device work (buffers are taken as addresses,

@@ -195,3 +195,21 @@ def test_page_resolution_under_sanitizers(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300,
                        env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0"))
     assert r.returncode == 0 and " 0 failure(s)" in r.stdout, (r.stdout + r.stderr)[-3000:]
+
+
+@pytest.mark.skipif(not os.path.exists("/opt/rocm/bin/hipcc"), reason="no ROCm toolchain")
+def test_no_attention_kernel_spills(tmp_path):
+    """Every instance keeps its state in registers: a spill would cost its speed, and spills of parts of matrix
+    operands have given wrong sums."""
+    from cross_model_kv_amd import build
+    asm = str(tmp_path / "q8_attend.s")
+    r = subprocess.run(["/opt/rocm/bin/hipcc", *build.HIP_FLAGS, "-S", "--offload-device-only",
+                        os.path.join(build.CSRC, "q8_attend.hip"), "-o", asm], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+    import re
+    src = open(asm).read()
+    names = re.findall(r"\.name: +(_ZN5kvmap\S+)", src)
+    assert len(names) >= 6
+    for field in ("private_segment_fixed_size", "vgpr_spill_count"):
+        sizes = [int(x) for x in re.findall(rf"\.{field}: +(\d+)", src)]
+        assert len(sizes) == len(names) and not any(sizes), dict(zip(names, sizes))
