@@ -199,8 +199,9 @@ struct Q8Attend {
 };
 // The launch of one attention call: fixed by the host's sizes alone.
 struct Q8Plan {
-    int nt, row_blocks;   // 16-row tiles of a workgroup, workgroups over a sequence's rows
-    int n_splits, tps;    // workgroups over its tokens, 64-token tiles of each
+    int nt, row_blocks;   // 16-row tiles of a workgroup, blocks of them over a sequence's rows
+    int grid;             // workgroups
+    bool splits;          // items may be cut: scratch and a second kernel
 };
 size_t q8_scratch_bytes(int cus);  // enough for every plan
 Q8Plan q8_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus);

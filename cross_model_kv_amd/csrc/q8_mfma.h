@@ -1,0 +1,126 @@
+// What the kernels that attend over the 8-bit cache share: e4m3 codes, queries and softmax weights as matrix
+// operands, and the constants of the running softmax.
+#pragma once
+
+#include "common.h"
+#include "internal.h"
+
+namespace kvmap {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -3.4028235e38f;  // the running maximum of a row that has seen no token
+constexpr float kSlack = 6.f;     // m is moved when a score passes it by this much (weights up to 2^6)
+
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float inf32() { return __uint_as_float(0x7F800000u); }
+__device__ __forceinline__ float nan32() { return __uint_as_float(0x7FC00000u); }
+
+template <bool BF16>
+struct Weights;  // what PV's operands are made of
+
+// 1 in every byte of w that is a NaN code
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7; }
+
+// 8 codes (two dwords) as a matrix operand
+__device__ __forceinline__ bf16x8_t bf16_codes(uint32_t a, uint32_t b) {
+    const bf16x2_t x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false);
+    const bf16x2_t x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true);
+    const bf16x2_t x2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false);
+    const bf16x2_t x3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true);
+    return bf16x8_t{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
+}
+__device__ __forceinline__ f16x8_t f16_codes(uint32_t a, uint32_t b) {
+    const f16x2_t x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, false);
+    const f16x2_t x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, true);
+    const f16x2_t x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, false);
+    const f16x2_t x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, true);
+    return f16x8_t{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
+}
+
+// x as a sum of three bf16 parts (8 bits each), exact to 2^-24
+struct Parts3 {
+    bf16x8_t p[3];
+    __device__ __forceinline__ void set(const float* x) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float rest = x[i];
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const __bf16 y = (__bf16)rest;
+                p[k][i] = y;
+                rest -= (float)y;
+            }
+        }
+    }
+};
+
+template <>
+struct Weights<true> {
+    using Codes = f16x8_t;
+    Codes p;
+    __device__ __forceinline__ void set(const float* x) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const f16x2_t y = __builtin_convertvector((f32x2_t{x[i], x[i + 1]}), f16x2_t);
+            p[i] = y[0];
+            p[i + 1] = y[1];
+        }
+    }
+    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b) { return f16_codes(a, b); }
+    __device__ __forceinline__ f32x4_t times(Codes v, f32x4_t o) const { return __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p, o, 0, 0, 0); }
+};
+template <>
+struct Weights<false> : Parts3 {
+    using Codes = bf16x8_t;
+    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b) { return bf16_codes(a, b); }
+    __device__ __forceinline__ f32x4_t times(Codes v, f32x4_t o) const {
+        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[2], o, 0, 0, 0);
+        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[1], o, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[0], o, 0, 0, 0);
+    }
+};
+
+template <bool BF16>
+struct Query;  // 8 dims of a query row as a matrix operand
+template <>
+struct Query<true> {
+    bf16x8_t p;
+    __device__ __forceinline__ void load(const void* base, int64_t at) { p = *(const bf16x8_t*)((const __bf16*)base + at); }
+    __device__ __forceinline__ void zero() { p = bf16x8_t{}; }
+    __device__ __forceinline__ f32x4_t times(bf16x8_t k, f32x4_t s) const { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, p, s, 0, 0, 0); }
+};
+template <>
+struct Query<false> : Parts3 {
+    __device__ __forceinline__ void load(const void* base, int64_t at) {
+        const float4 a = ((const float4*)((const float*)base + at))[0], b = ((const float4*)((const float*)base + at))[1];
+        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        set(x);
+    }
+    __device__ __forceinline__ void zero() { p[0] = p[1] = p[2] = bf16x8_t{}; }
+    __device__ __forceinline__ f32x4_t times(bf16x8_t k, f32x4_t s) const {
+        s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, p[2], s, 0, 0, 0);
+        s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, p[1], s, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, p[0], s, 0, 0, 0);
+    }
+};
+
+// 4 dims of one answered row, and at dim 0 its lse; a row whose weights sum to 0 saw no token.
+template <bool BF16>
+__device__ __forceinline__ void q8_store_row(const Q8Attend& a, int b, int i, int hq, int d4, float top, float lsum, f32x4_t sum) {
+    sum *= lsum == 0.f ? 0.f : 1.f / lsum;
+    const int64_t at = (int64_t)b * a.out.seq + (int64_t)hq * a.out.head + (int64_t)i * a.out.token + d4;
+    if (BF16)
+        *(uint2*)((uint16_t*)a.out.base + at) = make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
+    else
+        *(f32x4_t*)((float*)a.out.base + at) = sum;
+    if (d4 == 0 && a.lse)
+        a.lse[((int64_t)b * a.n_q + i) * a.Hq + hq] = lsum == 0.f ? -inf32() : (top + __builtin_amdgcn_logf(lsum)) * kLn2;
+}
+
+}  // namespace
+}  // namespace kvmap

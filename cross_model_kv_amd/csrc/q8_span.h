@@ -44,4 +44,9 @@ KVMAP_HD Q8Span q8_span(int64_t start, int64_t count, int64_t n, int64_t j, cons
     return s;
 }
 
+// Attention's steps over a sequence: at least one, also of an empty one and one whose length is out of range,
+// so that its rows are answered.
+constexpr int kQ8Step = 256;
+KVMAP_HD int q8_steps(int len, int max_len) { return len < 1 || len > max_len ? 1 : (len - 1) / kQ8Step + 1; }
+
 }  // namespace kvmap
