@@ -168,7 +168,7 @@ hipError_t launch_ridge_r2(int n, int p, int q, const RidgeSys* sys, double lamb
 hipError_t launch_fit_select(const double* r2, int L_src, int L_tgt, int H, int k, double* scores,
                              int32_t* sel, hipStream_t s);
 
-// ---- 8-bit paged cache (q8_pages.hip, q8_attend.hip) --------------------------------------
+// ---- 8-bit paged cache (q8_pages.hip, q8_attend.hip, q8_prompt.hip, q8_join.hip) --------------------------------------
 // Rows of d elements at base + layer/seq/head/token strides (elements).
 struct Q8Rows {
     void* base;
@@ -199,12 +199,32 @@ struct Q8Attend {
 };
 // The launch of one attention call: fixed by the host's sizes alone.
 struct Q8Plan {
-    int nt, row_blocks;   // 16-row tiles of a workgroup, blocks of them over a sequence's rows
-    int grid;             // workgroups
-    bool splits;          // items may be cut: scratch and a second kernel
+    int rows, row_blocks;  // rows of a workgroup, blocks of them over a sequence's rows
+    int grid;              // workgroups
+    bool splits;           // items may be cut: scratch and a second kernel
+    bool prompt;           // many rows: q8_prompt.hip's kernel
 };
+// Work is dealt out in steps of some tokens.  The steps of all items (sequence, KV head, row block), an item's own in
+// order, are one line of which every workgroup takes an equal piece: unequal lengths keep every CU busy, and the
+// split follows the lengths that the device holds, not max_len.  A piece that is not a whole item leaves its sums in a
+// slot, and a second kernel joins them.  (Joined in the first kernel by the last piece to arrive, the fences between the
+// XCDs' caches cost more than that launch: 526 us against 270 on 64 sequences of up to 16,384 tokens.)
+struct Q8Pieces {
+    int row_blocks, rows, grid;
+    bool few;        // no more items than pieces
+    int2* cut;       // [grid]: few: of an item, its first piece and their number; else of a piece, the item that it begins and
+                     // does not end, and the number of that item's pieces (1: there is none).  NULL: nothing is cut
+    float* part_o;   // [2 * grid][rows][d]: sums of pv times codes
+    float* part_ml;  // [2 * grid][rows][2]: m, l
+};
+Q8Pieces q8_pieces(const Q8Attend& a, const Q8Plan& p, void* scratch);
+size_t q8_piece_bytes(int grid, int rows, int d);
 size_t q8_scratch_bytes(int cus);  // enough for every plan
 Q8Plan q8_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus);
+// q8_prompt.hip's plan, or a plan with no rows where the call has too few of them.
+Q8Plan q8_prompt_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus);
+hipError_t launch_q8_prompt(Elem e, const Q8Attend& a, const Q8Pieces& sp, hipStream_t s);
+hipError_t launch_q8_join(Elem e, const Q8Attend& a, const Q8Pieces& sp, hipStream_t s);
 hipError_t launch_q8_attend(Elem e, const Q8Attend& a, const Q8Plan& p, void* scratch, hipStream_t s);
 // What a context keeps for these calls.
 struct Q8State {

@@ -36,19 +36,6 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = kQ8Step / kWaves;  // tokens of a wave's step
 
-// Work is dealt out in steps of kQ8Step tokens, a tile for each wave.  The steps of all items (sequence, KV head,
-// row block), an item's own in order, are one line of which every workgroup takes an equal piece: unequal
-// lengths keep every CU busy, and the split follows the lengths that the device holds, not max_len.  A piece
-// that is not a whole item leaves its sums in a slot, and a second kernel joins them, in the pieces' order.  (Joined in
-// the first kernel by the last piece to arrive, the fences between the XCDs' caches cost more than that launch:
-// 526 us against 270 on 64 sequences of up to 16,384 tokens.)
-struct Q8Split {
-    int row_blocks;
-    int grid;        // of the first kernel
-    float* part_o;   // [2 * grid][ROWS][d]: sums of pv times codes
-    float* part_ml;  // [2 * grid][ROWS][2]: m, l
-};
-
 // One tile's codes as loaded: keys of 4 x 16 tokens, values of D dims, and the lane's scales (the
 // tokens 16 g .. 16 g + 15 lie in one page, pages being whole 16 tokens).
 template <int D>
@@ -63,10 +50,6 @@ struct TileData {
 // stops at two row tiles and a test reads every instance's scratch size.
 template <bool BF16, int D, int NT>
 constexpr int kOccupancy = !BF16 ? (NT == 1 ? 2 : 1) : NT == 1 ? 3 : NT == 2 ? 2 : 1;
-
-__device__ __forceinline__ uint64_t div64(uint64_t a, uint64_t b) {
-    return (a | b) >> 32 ? a / b : (uint64_t)((uint32_t)a / (uint32_t)b);
-}
 
 // Sums of the lanes up to and including one's own.
 __device__ __forceinline__ uint32_t wave_scan(uint32_t x, int lane) {
@@ -107,7 +90,7 @@ __device__ __forceinline__ uint64_t steps_between(const Q8Attend& a, int first, 
 }
 
 template <bool BF16, int D, int NT>
-__global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kernel(Q8Attend a, Q8Split sp) {
+__global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kernel(Q8Attend a, Q8Pieces sp) {
     constexpr int ROWS = 16 * NT;
     constexpr int LDO = D + 4;
     __shared__ float s_o[kWaves][ROWS][LDO];
@@ -126,6 +109,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
     const uint64_t share = div64(total + gridDim.x - 1, gridDim.x);
     uint64_t at = share * blockIdx.x;
     const uint64_t stop = at + share < total ? at + share : total;
+    if (tid == 0 && sp.cut && !sp.few) sp.cut[blockIdx.x] = make_int2(0, 1);
     if (at >= stop) return;
     int b = 0;
     uint64_t base = 0;  // the sequence's first step
@@ -389,9 +373,12 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
         __syncthreads();
         const int rows = min(ROWS, R - rb * ROWS);
         asm volatile("" : "+v"(x0));  // (nor across the loop above)
+        if (x0 == 0 && sp.cut && s_begin == 0) {  // (of several items that begin here only the last may be cut)
+            const int pieces = (int)div64(item_at + steps - 1, share) - (int)blockIdx.x + 1, id = b * items + item;
+            sp.cut[sp.few ? id : (int)blockIdx.x] = make_int2(sp.few ? (int)blockIdx.x : id, pieces);
+        }
         if (s_begin > 0 || s_end < steps) {
-            // slot 2 w + 1 is for an item's first piece (w's last), 2 w for any other (w's first)
-            const int64_t slot = (2 * (int64_t)blockIdx.x + (s_begin == 0)) * ROWS;
+            const int64_t slot = q8_slot(blockIdx.x, s_begin == 0) * ROWS;
             for (int x = x0; x < rows * (D / 4); x += 256) {
                 const int row = x / (D / 4), d4 = x % (D / 4) * 4;
                 float top, lsum;
@@ -416,117 +403,49 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
     }
 }
 
-// The pieces of one row joined, in order; a row of an item of one piece has its answer already.
-template <bool BF16, int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void q8_join_kernel(Q8Attend a, Q8Split sp, int block_rows) {
-    constexpr int LANES = D / 4, NG = 64 * WAVES / LANES;  // groups of threads that take the pieces in turn
-    constexpr int U = WAVES == 1 ? 16 : 8;          // pieces in flight
-    __shared__ f32x4_t s_o[NG][LANES];
-    __shared__ float s_ml[NG][2];
-    const int G = a.Hq / a.c.H, items = a.c.H * sp.row_blocks;
-    const int tid = threadIdx.x, lane = tid & 63, group = tid / LANES, d4 = tid % LANES * 4;
-    const int r = blockIdx.x, b = blockIdx.y / a.c.H, h = blockIdx.y % a.c.H;
-    const int steps = q8_steps(a.len[b], a.max_len);
-    if (steps == 1) return;
-    const uint64_t before = steps_between(a, 0, b, lane), total = (before + steps_between(a, b, a.B, lane)) * items;
-    const uint64_t share = div64(total + sp.grid - 1, sp.grid);
-    const uint64_t item_at = before * items + (uint64_t)(h * sp.row_blocks + r / block_rows) * steps;
-    const int w0 = (int)div64(item_at, share), n = (int)div64(item_at + steps - 1, share) - w0 + 1;
-    if (n == 1) return;
-    float top = kNone, lsum = 0.f;
-    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = group; j0 < n; j0 += U * NG) {
-        float2 ml[U];
-        f32x4_t po[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int w = min(j0 + u * NG, n - 1);
-            const int64_t from = (2 * (int64_t)(w0 + w) + (w == 0)) * block_rows + r % block_rows;
-            ml[u] = *(const float2*)(sp.part_ml + from * 2);
-            po[u] = *(const f32x4_t*)(sp.part_o + from * D + d4);
-        }
-        float t = top;
-#pragma unroll
-        for (int u = 0; u < U; ++u) t = fmaxf(t, ml[u].x);
-        const float keep = __builtin_amdgcn_exp2f(top - t);
-        lsum *= keep;
-        sum *= keep;
-        top = t;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (j0 + u * NG < n) {
-                const float f = __builtin_amdgcn_exp2f(ml[u].x - t);
-                lsum = fmaf(f, ml[u].y, lsum);
-                sum += f * po[u];
-            }
-    }
-    s_o[group][tid % LANES] = sum;
-    if (d4 == 0) {
-        s_ml[group][0] = top;
-        s_ml[group][1] = lsum;
-    }
-    __syncthreads();
-    if (group) return;
-    top = s_ml[0][0];
-#pragma unroll
-    for (int k = 1; k < NG; ++k) top = fmaxf(top, s_ml[k][0]);
-    lsum = 0.f;
-    sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < NG; ++k) {
-        const float f = __builtin_amdgcn_exp2f(s_ml[k][0] - top);
-        lsum = fmaf(f, s_ml[k][1], lsum);
-        sum += f * s_o[k][tid];
-    }
-    q8_store_row<BF16>(a, b, r / G, h * G + r % G, d4, top, lsum, sum);
-}
-
 // Row tiles of a workgroup: as many as the rows fill and the registers hold.
 int row_tiles(int64_t R, bool bf16, int d) { return R <= 16 ? 1 : R <= 32 || !bf16 || d > 64 ? 2 : 4; }
 
 // Workgroups that a CU holds at once, as the registers (kOccupancy) and the shared memory allow.
 constexpr int per_cu(bool bf16, int nt) { return bf16 ? (nt == 1 ? 3 : nt == 2 ? 2 : 1) : (nt == 1 ? 2 : 1); }
-constexpr int kSlotRows = 64;  // the most of per_cu * 16 * nt
 
 }  // namespace
 
 Q8Plan q8_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus) {
-    Q8Plan p;
+    Q8Plan p = q8_prompt_plan(e, B, n_q, Hq, H, d, max_len, cus);
+    if (p.rows) return p;
     const int64_t R = (int64_t)n_q * (Hq / H);
-    p.nt = row_tiles(R, e == Elem::BF16, d);
-    p.row_blocks = (int)((R + 16 * p.nt - 1) / (16 * p.nt));
+    const int nt = row_tiles(R, e == Elem::BF16, d);
+    p.rows = 16 * nt;
+    p.row_blocks = (int)((R + p.rows - 1) / p.rows);
     // a workgroup for every step that the lengths can bring, up to what the chip holds at once
     const double steps = (double)B * H * p.row_blocks * q8_steps(max_len, max_len);
-    p.grid = (int)std::min<double>((double)per_cu(e == Elem::BF16, p.nt) * cus, steps);
+    p.grid = (int)std::min<double>((double)per_cu(e == Elem::BF16, nt) * cus, steps);
     p.splits = p.grid > 1 && q8_steps(max_len, max_len) > 1;  // (items of one step are never cut)
     return p;
 }
 
-// Two slots of a workgroup.
-size_t q8_scratch_bytes(int cus) { return (size_t)2 * cus * kSlotRows * (128 + 2) * sizeof(float); }
+size_t q8_scratch_bytes(int cus) {
+    // the most rows of all workgroups together: 256 a CU (q8_prompt.hip); the most workgroups: 3 a CU
+    return q8_piece_bytes(3 * cus, 0, 128) + q8_piece_bytes(cus, 256, 128);
+}
 
 template <bool BF16, int D>
-static hipError_t launch_attend(const Q8Attend& a, const Q8Plan& p, void* scratch, hipStream_t s) {
-    const int rows = 16 * p.nt;
-    const Q8Split sp{p.row_blocks, p.grid, (float*)scratch, (float*)scratch + (size_t)2 * p.grid * rows * D};
-    const dim3 grid((unsigned)p.grid);
-    if (p.nt == 1) hipLaunchKernelGGL((q8_decode_kernel<BF16, D, 1>), grid, dim3(256), 0, s, a, sp);
-    else if (p.nt == 2) hipLaunchKernelGGL((q8_decode_kernel<BF16, D, 2>), grid, dim3(256), 0, s, a, sp);
+static hipError_t launch_decode(const Q8Attend& a, const Q8Pieces& sp, hipStream_t s) {
+    const dim3 grid((unsigned)sp.grid);
+    if (sp.rows == 16) hipLaunchKernelGGL((q8_decode_kernel<BF16, D, 1>), grid, dim3(256), 0, s, a, sp);
+    else if (sp.rows == 32) hipLaunchKernelGGL((q8_decode_kernel<BF16, D, 2>), grid, dim3(256), 0, s, a, sp);
     else if constexpr (BF16 && D == 64) hipLaunchKernelGGL((q8_decode_kernel<BF16, D, 4>), grid, dim3(256), 0, s, a, sp);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !p.splits) return e;
-    // Many rows have few pieces each, and a wave is enough for one; few rows may have hundreds.  (512 items of 8 rows:
-    // 14.4 us with four waves each, 11.0 with one; 8 items of 8 rows
-    // in 96 pieces: 4.6 us with four.)
-    const dim3 jobs((unsigned)(a.n_q * (a.Hq / a.c.H)), (unsigned)(a.B * a.c.H));
-    if ((int64_t)jobs.x * jobs.y >= 1024) hipLaunchKernelGGL((q8_join_kernel<BF16, D, 1>), jobs, dim3(64), 0, s, a, sp, rows);
-    else hipLaunchKernelGGL((q8_join_kernel<BF16, D, 4>), jobs, dim3(256), 0, s, a, sp, rows);
     return hipGetLastError();
 }
 
 hipError_t launch_q8_attend(Elem e, const Q8Attend& a, const Q8Plan& p, void* scratch, hipStream_t s) {
-    if (e == Elem::BF16) return a.c.d == 128 ? launch_attend<true, 128>(a, p, scratch, s) : launch_attend<true, 64>(a, p, scratch, s);
-    return a.c.d == 128 ? launch_attend<false, 128>(a, p, scratch, s) : launch_attend<false, 64>(a, p, scratch, s);
+    const Q8Pieces sp = q8_pieces(a, p, scratch);
+    hipError_t r;
+    if (p.prompt) r = launch_q8_prompt(e, a, sp, s);
+    else if (e == Elem::BF16) r = a.c.d == 128 ? launch_decode<true, 128>(a, sp, s) : launch_decode<true, 64>(a, sp, s);
+    else r = a.c.d == 128 ? launch_decode<false, 128>(a, sp, s) : launch_decode<false, 64>(a, sp, s);
+    return r == hipSuccess && p.splits ? launch_q8_join(e, a, sp, s) : r;
 }
 
 }  // namespace kvmap

@@ -11,7 +11,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3.4028235e38f;  // the running maximum of a row that has seen no token
-constexpr float kSlack = 6.f;     // m is moved when a score passes it by this much (weights up to 2^6)
+constexpr float kSlack = 14.f;   // m is moved when a score passes it by more than this: weights reach 2^14, fp16 65504
 
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -26,36 +26,38 @@ struct Weights;  // what PV's operands are made of
 // 1 in every byte of w that is a NaN code
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7; }
 
-// 8 codes (two dwords) as a matrix operand
-__device__ __forceinline__ bf16x8_t bf16_codes(uint32_t a, uint32_t b) {
-    const bf16x2_t x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false);
-    const bf16x2_t x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true);
-    const bf16x2_t x2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false);
-    const bf16x2_t x3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true);
+// 8 codes (two dwords) as a matrix operand, times a power of two
+__device__ __forceinline__ bf16x8_t bf16_codes(uint32_t a, uint32_t b, float by = 1.f) {
+    const bf16x2_t x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, by, false);
+    const bf16x2_t x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, by, true);
+    const bf16x2_t x2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, by, false);
+    const bf16x2_t x3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, by, true);
     return bf16x8_t{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
 }
-__device__ __forceinline__ f16x8_t f16_codes(uint32_t a, uint32_t b) {
-    const f16x2_t x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, false);
-    const f16x2_t x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, true);
-    const f16x2_t x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, false);
-    const f16x2_t x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, true);
+__device__ __forceinline__ f16x8_t f16_codes(uint32_t a, uint32_t b, float by = 1.f) {
+    const f16x2_t x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, by, false);
+    const f16x2_t x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, by, true);
+    const f16x2_t x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, by, false);
+    const f16x2_t x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, by, true);
     return f16x8_t{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
 }
 
 // x as a sum of three bf16 parts (8 bits each), exact to 2^-24
 struct Parts3 {
     bf16x8_t p[3];
+    __device__ __forceinline__ void put(int i, float x0, float x1) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const bf16x2_t y = __builtin_convertvector((f32x2_t{x0, x1}), bf16x2_t);
+            p[k][i] = y[0];
+            p[k][i + 1] = y[1];
+            x0 -= (float)y[0];
+            x1 -= (float)y[1];
+        }
+    }
     __device__ __forceinline__ void set(const float* x) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float rest = x[i];
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                const __bf16 y = (__bf16)rest;
-                p[k][i] = y;
-                rest -= (float)y;
-            }
-        }
+        for (int i = 0; i < 8; i += 2) put(i, x[i], x[i + 1]);
     }
 };
 
@@ -63,27 +65,64 @@ template <>
 struct Weights<true> {
     using Codes = f16x8_t;
     Codes p;
+    __device__ __forceinline__ void put(int i, float x0, float x1) {
+        const f16x2_t y = __builtin_convertvector((f32x2_t{x0, x1}), f16x2_t);
+        p[i] = y[0];
+        p[i + 1] = y[1];
+    }
     __device__ __forceinline__ void set(const float* x) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const f16x2_t y = __builtin_convertvector((f32x2_t{x[i], x[i + 1]}), f16x2_t);
-            p[i] = y[0];
-            p[i + 1] = y[1];
-        }
+        for (int i = 0; i < 8; i += 2) put(i, x[i], x[i + 1]);
     }
-    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b) { return f16_codes(a, b); }
+    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b, float by = 1.f) { return f16_codes(a, b, by); }
     __device__ __forceinline__ f32x4_t times(Codes v, f32x4_t o) const { return __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p, o, 0, 0, 0); }
+    __device__ __forceinline__ f32x16_t times(Codes v, f32x16_t o) const { return __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p, o, 0, 0, 0); }
 };
 template <>
 struct Weights<false> : Parts3 {
     using Codes = bf16x8_t;
-    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b) { return bf16_codes(a, b); }
+    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b, float by = 1.f) { return bf16_codes(a, b, by); }
     __device__ __forceinline__ f32x4_t times(Codes v, f32x4_t o) const {
         o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[2], o, 0, 0, 0);
         o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[1], o, 0, 0, 0);
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[0], o, 0, 0, 0);
     }
+    __device__ __forceinline__ f32x16_t times(Codes v, f32x16_t o) const {
+        o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[2], o, 0, 0, 0);
+        o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[1], o, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[0], o, 0, 0, 0);
+    }
 };
+
+// s (+)= k q with s in vector registers and q in accumulation registers.  Where a kernel may use accumulation registers the
+// compiler puts every product's result there, and moves what vector instructions need of it, one register an instruction:
+// a quarter of the vector work of a tile.  Written out, the compiler does not know that it is a matrix product, whose result
+// may not be read by a vector instruction within 11 instructions (8 passes): the caller keeps them apart, and
+// tests/test_q8_boundary.py reads the listing for it.
+template <bool FIRST>
+__device__ __forceinline__ void mfma_to_vector(bf16x8_t k, bf16x8_t q, f32x16_t& s) {
+    if (FIRST) asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(s) : "v"(k), "a"(q));
+    else asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(k), "a"(q));
+}
+
+// Puts q where mfma_to_vector takes it from, once and for all: copied there in front of a use, it would not be there in time.
+template <class T>
+__device__ __forceinline__ void keep_accumulated(T& q) { asm volatile("" : "+a"(q)); }
+
+// From here on vector instructions may read s.
+__device__ __forceinline__ void product_done(f32x16_t& s) { asm volatile("s_nop 15" : "+v"(s)); }
+
+// o *= by, o in accumulation registers.  (As plain arithmetic in a branch, the compiler moves all of o to vector registers in
+// front of the branch, taken or not.)
+__device__ __forceinline__ void scale_product(f32x16_t& o, float by) {
+    asm volatile("s_nop 15" : "+a"(o));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float x = o[i], t;
+        asm volatile("v_accvgpr_read_b32 %1, %0\n\tv_mul_f32 %1, %2, %1\n\tv_accvgpr_write_b32 %0, %1" : "+a"(x), "=&v"(t) : "v"(by));
+        o[i] = x;
+    }
+}
 
 template <bool BF16>
 struct Query;  // 8 dims of a query row as a matrix operand
@@ -93,6 +132,11 @@ struct Query<true> {
     __device__ __forceinline__ void load(const void* base, int64_t at) { p = *(const bf16x8_t*)((const __bf16*)base + at); }
     __device__ __forceinline__ void zero() { p = bf16x8_t{}; }
     __device__ __forceinline__ f32x4_t times(bf16x8_t k, f32x4_t s) const { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, p, s, 0, 0, 0); }
+    __device__ __forceinline__ f32x16_t times(bf16x8_t k, f32x16_t s) const { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, p, s, 0, 0, 0); }
+    __device__ __forceinline__ void keep() { keep_accumulated(p); }
+    // s (+)= k times the queries, s in vector registers.
+    template <bool FIRST>
+    __device__ __forceinline__ void to_vector(bf16x8_t k, f32x16_t& s) const { mfma_to_vector<FIRST>(k, p, s); }
 };
 template <>
 struct Query<false> : Parts3 {
@@ -107,7 +151,30 @@ struct Query<false> : Parts3 {
         s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, p[1], s, 0, 0, 0);
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, p[0], s, 0, 0, 0);
     }
+    __device__ __forceinline__ f32x16_t times(bf16x8_t k, f32x16_t s) const {
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, p[2], s, 0, 0, 0);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, p[1], s, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, p[0], s, 0, 0, 0);
+    }
+    __device__ __forceinline__ void keep() {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) keep_accumulated(p[k]);
+    }
+    template <bool FIRST>
+    __device__ __forceinline__ void to_vector(bf16x8_t k, f32x16_t& s) const {
+        mfma_to_vector<FIRST>(k, p[2], s);
+        mfma_to_vector<false>(k, p[1], s);
+        mfma_to_vector<false>(k, p[0], s);
+    }
 };
+
+// Division with the usual case of small numbers in 32 bits.
+__device__ __forceinline__ uint64_t div64(uint64_t a, uint64_t b) {
+    return (a | b) >> 32 ? a / b : (uint64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// A piece's slots: one for an item that it begins (its last), one for an item that began before (its first).
+__host__ __device__ __forceinline__ int64_t q8_slot(int64_t piece, bool begins) { return 2 * piece + begins; }
 
 // 4 dims of one answered row, and at dim 0 its lse; a row whose weights sum to 0 saw no token.
 template <bool BF16>

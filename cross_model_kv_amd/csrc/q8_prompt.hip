@@ -1,0 +1,547 @@
+// Attention over the 8-bit paged cache for many rows: prompts (the mathematics is q8_attend.hip's).
+//
+// A workgroup of 8 waves holds 256 rows of one sequence and KV head (row r = i * G + g, query i, head g), a wave 32 of them, and
+// walks the tokens in tiles of 64.  A tile's codes are turned to 16 bits once for the workgroup, on their way into
+// shared memory, and every wave reads all of it as the left operand:
+//   S^T = K Q^T   A = 32 tokens x 16 dims,  B = 16 dims x 32 rows   (32x32x16 tiles; queries stay in registers)
+//   O^T = V^T P^T A = 32 dims x 16 tokens,  B = 16 tokens x 32 rows
+// Row m of S^T's 32 tokens is token (m & 3) + 4 (m >> 3) + 16 (m >> 2 & 1), so that a lane's 16 scores of a row
+// are 16 adjacent tokens, which is what P^T's operand wants of it: nothing crosses lanes, and the 16
+// tokens lie in one page, with one scale.
+//
+// What bounds it: a tile costs a SIMD (64 rows) 2054 cycles of matrix products, 2215 of issuing vector instructions
+// (these among them) and takes 4090; the clock meanwhile falls to 1.6 - 1.8 GHz.  Waves of 64 rows, one a SIMD, read
+// half as much shared memory but cannot issue fast enough (an instruction every 5 cycles, 580 of them a tile): 4400
+// cycles at a clock as much higher, the same 1.15 - 1.18 ms for 8,192 rows a head, 8 heads and 33,792 tokens (950 TFLOP/s, against
+// 1430 - 1550 of large library products here).  32 products of the wave next to the vector work in the order
+// in which they are written, not the compiler's, took that from 1470 us (64 rows) to 1180.
+
+#include <algorithm>
+#include <utility>
+
+#include "common.h"
+#include "internal.h"
+#include "q8_mfma.h"
+#include "q8_span.h"
+
+namespace kvmap {
+namespace {
+
+// f(integral_constant<0>), .., f(integral_constant<N - 1>): unrolled whatever f's body looks like.
+template <int... I, class F>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F&& f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+    each(std::make_integer_sequence<int, N>{}, f);
+}
+
+constexpr int kTile = 64;
+#define STEP() __builtin_amdgcn_sched_barrier(0)
+
+// Tokens that the last row of a row block sees, and its tiles: one at least, so that its rows are answered.
+__device__ __forceinline__ int block_end(const Q8Attend& a, int G, int len, int rb, int bm) {
+    const int last = min((rb + 1) * bm, a.n_q * G) - 1;
+    return len - a.n_q + last / G + 1;
+}
+__device__ __forceinline__ int block_tiles(const Q8Attend& a, int G, int len, int rb, int bm) {
+    if (len < 1 || len > a.max_len) return 1;
+    const int end = block_end(a, G, len, rb, bm);
+    return end < 1 ? 1 : (end - 1) / kTile + 1;
+}
+__device__ __forceinline__ uint64_t wave_scan(uint64_t x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint64_t y = __shfl_up((unsigned long long)x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+__device__ __forceinline__ uint64_t last_lane(uint64_t x) { return __shfl((unsigned long long)x, 63); }
+// Tiles of all row blocks of one head: of sequence b0 + lane (0 past the last), lanes going over the sequences or over the row
+// blocks, whichever is fewer rounds.
+__device__ __forceinline__ uint64_t head_tiles(const Q8Attend& a, int G, int b0, int row_blocks, int bm, int lane) {
+    uint64_t sum = 0;
+    const int n = min(a.B - b0, 64);
+    if (n * ((row_blocks + 63) / 64) < row_blocks) {
+        for (int i = 0; i < n; ++i) {
+            const int len = a.len[b0 + i];
+            uint64_t s = 0;
+            for (int r0 = 0; r0 < row_blocks; r0 += 64)
+                s += last_lane(wave_scan(r0 + lane < row_blocks ? block_tiles(a, G, len, r0 + lane, bm) : 0, lane));
+            if (i == lane) sum = s;
+        }
+    } else if (lane < n) {
+        const int len = a.len[b0 + lane];
+        for (int rb = 0; rb < row_blocks; ++rb) sum += block_tiles(a, G, len, rb, bm);
+    }
+    return sum;
+}
+
+// An item, and where it lies in the line.
+struct Item {
+    int b, h, rb, tiles;
+    uint64_t at;
+};
+// The line's length, and the item that holds its tile u (u < the length): every lane of the wave alike.
+__device__ __forceinline__ uint64_t line_length(const Q8Attend& a, int G, int row_blocks, int bm, int lane) {
+    uint64_t total = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) total += last_lane(wave_scan(head_tiles(a, G, b0, row_blocks, bm, lane), lane));
+    return total * a.c.H;
+}
+__device__ __forceinline__ bool find_item(const Q8Attend& a, int G, int row_blocks, int bm, int lane, uint64_t u, Item& it) {
+    uint64_t base = 0, head = 0;
+    for (int b0 = 0;; b0 += 64) {
+        if (b0 >= a.B) return false;  // (not reached while the lengths stay as they were summed)
+        const uint64_t mine = head_tiles(a, G, b0, row_blocks, bm, lane);
+        const uint64_t upto = wave_scan(mine, lane) * a.c.H;
+        const uint64_t past = __ballot(base + upto > u);
+        if (past) {
+            const int n = __ffsll((unsigned long long)past) - 1;
+            it.b = b0 + n;
+            head = __shfl((unsigned long long)mine, n);
+            base += __shfl((unsigned long long)upto, n) - head * a.c.H;
+            break;
+        }
+        base += last_lane(upto);
+    }
+    it.h = (int)div64(u - base, head);
+    base += (uint64_t)it.h * head;
+    const int len = a.len[it.b];
+    for (int r0 = 0;; r0 += 64) {
+        if (r0 >= row_blocks) return false;  // (as above)
+        const uint64_t mine = r0 + lane < row_blocks ? block_tiles(a, G, len, r0 + lane, bm) : 0;
+        const uint64_t upto = wave_scan(mine, lane);
+        const uint64_t past = __ballot(base + upto > u);
+        if (past) {
+            const int n = __ffsll((unsigned long long)past) - 1;
+            it.rb = r0 + n;
+            it.tiles = (int)__shfl((unsigned long long)mine, n);
+            it.at = base + __shfl((unsigned long long)upto, n) - it.tiles;
+            break;
+        }
+        base += last_lane(upto);
+    }
+    return true;
+}
+
+// The lane, computed where it is wanted: registers are full, and the compiler would hold it, and its products with strides,
+// across loops.
+__device__ __forceinline__ int fresh_lane() {
+    int lane;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(lane));
+    return lane;
+}
+
+template <bool BF16, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q8_prompt_kernel(Q8Attend a, Q8Pieces sp) {
+    constexpr int BM = 32 * WAVES;             // rows of a workgroup
+    constexpr int KROW = 2 * D + 16;           // bytes of a token's keys in shared memory: the 16 spread the banks
+    constexpr int KBYTES = kTile * KROW;
+    constexpr int VROW = 2 * kTile + 16;       // bytes of a dim's tokens
+    constexpr int THREADS = 64 * WAVES;
+    constexpr int NC = D * kTile / 16 / THREADS;  // 16-byte loads of a thread for a tile's keys, and for its values
+    constexpr int NQ = D / 8, NV = D / 8;      // operands of a tile: keys, values
+    constexpr int AHEAD = 3;
+    constexpr int CPT = D / 16;                // such loads of a token's keys
+    __shared__ __align__(16) uint8_t s_k[3 * KBYTES];
+    __shared__ __align__(16) uint8_t s_v[2][D * VROW];
+    __shared__ int s_nan;                      // some value was taken out
+    __shared__ float2 s_scale[4][4];           // k_scale, v_scale of 16 tokens each; a tile's are written with its keys
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int G = a.Hq / a.c.H, R = a.n_q * G;
+    const int P = a.c.page, logP = 31 - __clz(P);
+    const float y2 = a.scale * kLog2e;
+
+    // this workgroup's piece; those of one XCD (workgroups 8 apart) are neighbours, which share a head's keys and values
+    const int piece = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
+    const uint64_t total = line_length(a, G, sp.row_blocks, BM, fresh_lane());
+    const uint64_t share = div64(total + sp.grid - 1, sp.grid);
+    uint64_t at = share * piece;
+    const uint64_t stop = at + share < total ? at + share : total;
+    if (threadIdx.x == 0 && sp.cut && !sp.few) sp.cut[piece] = make_int2(0, 1);
+
+    while (at < stop) {
+        Item it;
+        if (!find_item(a, G, sp.row_blocks, BM, fresh_lane(), at, it)) return;
+        const int b = __builtin_amdgcn_readfirstlane(it.b), h = __builtin_amdgcn_readfirstlane(it.h);
+        const int rb = __builtin_amdgcn_readfirstlane(it.rb);
+        const int len = a.len[b];
+        const bool bad = len < 0 || len > a.max_len;
+        const int t0 = __builtin_amdgcn_readfirstlane((int)(at - it.at));
+        const int t1 = __builtin_amdgcn_readfirstlane((int)min((uint64_t)it.tiles, stop - it.at));
+        const int first_end = bad ? 0 : len - a.n_q + rb * BM / G + 1;               // the fewest tokens that a row sees
+        const int wave_end = bad ? 0 : len - a.n_q + (rb * BM + wave * 32) / G + 1;  // the same of the wave's rows
+        const int32_t* pages = a.pages + (int64_t)b * a.max_pages;
+
+        const int tid = 64 * wave + fresh_lane(), c = tid & 31, hi = tid >> 5 & 1;
+        Query<BF16> q[D / 16];
+        const int row = rb * BM + wave * 32 + c;  // of the sequence and head
+        const int end = bad ? 0 : min(len - a.n_q + row / G + 1, len);
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st) {
+            if (row < R)
+                q[st].load(a.q.base, (int64_t)b * a.q.seq + (int64_t)(h * G + row % G) * a.q.head + (int64_t)(row / G) * a.q.token + 16 * st + 8 * hi);
+            else
+                q[st].zero();
+            q[st].keep();
+        }
+        f32x16_t o[D / 32];
+        float m = kNone, l = 0.f;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+            keep_accumulated(o[d]);
+        }
+
+        // A thread's part of a tile: keys as 16 dims of the tokens ktok(j), values as 16 tokens (group tid & 3) of the dims
+        // vdim(j), and the group's scales.
+        auto ktok = [&](int j) { return (tid + THREADS * j) / CPT; };
+        auto wave_tok = [&](int j) { return (64 * wave + THREADS * j) / CPT; };  // the wave's first: all of them lie in one page
+        auto vdim = [&](int j) { return (tid + THREADS * j) / 4; };
+        // The table's entry of a token, and that entry checked: apart, because a check waits for the load.  Without a branch,
+        // because the main loop's body has to stay one block.
+        auto entry_of = [&](int tok) { return pages[min(tok >> logP, a.max_pages - 1)]; };
+        auto page_of = [&](int tok, int p) { return (tok >> logP) < a.max_pages && p >= 0 && p < a.c.n_pages ? p : -1; };
+        const uint8_t *kh = a.c.k + (int64_t)h * P * D, *vh = a.c.v + (int64_t)h * P * D;
+        const float *ksh = a.c.ks + h, *vsh = a.c.vs + h;
+        const uint32_t page_bytes = a.c.H * P * D;  // of all heads (H < 2^16)
+        u32x4_t kx[NC], vx[NC];
+        int pk[NC], pg, pv, ps;
+        float2 sc;
+        auto find_pages = [&](int tile) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) pk[j] = entry_of(tile * kTile + wave_tok(j));
+            pg = entry_of(tile * kTile + 16 * (tid & 3));
+        };
+        uint32_t koff[NC], voff;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) koff[j] = (ktok(j) & (P - 1)) * D + 16 * (tid % CPT);
+        voff = (16 * (tid & 3) & (P - 1)) + vdim(0) * P;
+        auto load_k = [&](int tile) {
+            const uint8_t* at = kh + ((tile * kTile) & (P - 1)) * D;  // (64 tokens begin a page, or the second half of one)
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+                kx[j] = *(const u32x4_t*)(at + (uint64_t)(uint32_t)max(page_of(tile * kTile + wave_tok(j), __builtin_amdgcn_readfirstlane(pk[j])), 0) * page_bytes + koff[j]);
+            pv = page_of(tile * kTile + 16 * (tid & 3), pg);
+            const uint64_t g = (uint64_t)(uint32_t)max(pv, 0) * (uint32_t)a.c.H;
+            sc = make_float2(ksh[g], vsh[g]);
+            ps = pv;
+        };
+        auto load_v = [&](int tile) {
+            const uint8_t* v = vh + ((tile * kTile) & (P - 1)) + ((uint64_t)(uint32_t)max(pv, 0) * page_bytes + voff);
+#pragma unroll
+            for (int j = 0; j < NC; ++j) vx[j] = *(const u32x4_t*)(v + THREADS / 4 * j * P);
+        };
+        auto store_k = [&](int at) {
+            uint8_t* to = s_k + at;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                const int t = ktok(j), row = (t & 32) + (t & 3) + 4 * (t >> 4 & 1) + 8 * (t >> 2 & 3);
+                bf16x8_t* w = (bf16x8_t*)(to + row * KROW + 32 * (tid % CPT));
+                w[0] = bf16_codes(kx[j][0], kx[j][1]);
+                w[1] = bf16_codes(kx[j][2], kx[j][3]);
+            }
+        };
+        auto store_scale = [&](int tile) {
+            // a page out of range makes the scores that need it NaN; past the sequence's end there is no page
+            if (tid < 4) s_scale[tile & 3][tid] = ps < 0 || tile * kTile + 16 * tid >= len ? make_float2(nan32(), 1.f) : sc;
+        };
+        uint32_t hidden_nan = 0;
+        if (tid == 0) s_nan = 0;
+        auto clean_v = [&](int tile) {
+            if (tile * kTile + kTile <= first_end) return;
+            // codes past the sequence's end may be anything: they become zeros, since 0 times NaN is NaN; and so do
+            // NaN codes that some of the rows do not see, which is put right after the loop
+            const int nv = min(max(len - tile * kTile - 16 * (tid & 3), 0), 16);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const int nb = nv - 4 * z;
+                const uint32_t keep = nb >= 4 ? 0xFFFFFFFFu : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
+#pragma unroll
+                for (int j = 0; j < NC; ++j) {
+                    vx[j][z] &= keep;
+                    const uint32_t bits = nan_codes(vx[j][z]);
+                    hidden_nan |= bits;
+                    vx[j][z] &= ~(bits * 0xFFu);
+                }
+            }
+        };
+        float vs_next;  // the scale of the values that this stores
+        auto store_v = [&](int tile) {
+            uint8_t* to = s_v[tile & 1];
+            const int ev = (int)(__float_as_uint(vs_next) >> 23) - 127;
+            const float small = ev < -90 ? vs_next * 0x1p90f : 1.f;  // (see bias below)
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                auto* w = (typename Weights<BF16>::Codes*)(to + vdim(j) * VROW + 32 * (tid & 3));
+                w[0] = Weights<BF16>::codes(vx[j][0], vx[j][1], small);
+                w[1] = Weights<BF16>::codes(vx[j][2], vx[j][3], small);
+            }
+        };
+
+        // The walk goes by halves of a tile, 32 tokens: half 2 t + mt is tokens 32 mt .. of tile t.  Scores of a half: token
+        // 16 hi + i in x[n][i].
+        f32x16_t even, odd;    // of the halves 2 t and 2 t + 1
+        float top;             // the largest of the half that comes next
+        float cs, bias, back;  // its scales, made of
+        float2 scl;
+        int k_at = 0, k_next = KBYTES, k_last = 2 * KBYTES;  // where tiles t, t + 1, t + 2 keep their keys
+        auto read_scale = [&](int tile, int mt) { scl = s_scale[tile & 3][2 * mt + hi]; };
+        auto use_scale = [&]() {
+            const int ev = (int)(__float_as_uint(scl.y) >> 23) - 127;
+            cs = scl.x * y2;
+            bias = (float)max(ev, -90);  // (values under 2^-82: l would overflow on their 1 / v_scale)
+            back = __uint_as_float((uint32_t)(127 - max(ev, -90)) << 23);  // 1 / v_scale
+        };
+        // The mask, where some row of the wave does not see all of the half; and the maximum moved where a score passes it by more
+        // than kSlack.
+        auto settle = [&](auto FIRST, int tile, int mt, f32x16_t& x) {
+            const int from = tile * kTile + 32 * mt;
+            if (from + 32 > wave_end) {
+                const int see = end - from - 16 * hi;
+                top = -inf32();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    x[i] = i < see ? fmaf(x[i], cs, bias) : -inf32();
+                    top = fmaxf(top, x[i]);
+                }
+                cs = 1.f;
+                bias = 0.f;
+            }
+            float t = fmaf(top, cs, bias);
+            if (__any(t > m + kSlack)) {
+                t = fmaxf(fmaxf(t, __shfl_xor(t, 32)), m);
+                const float keep = __builtin_amdgcn_exp2f(m - t);
+                m = t;
+                if constexpr (!FIRST) {  // (nothing is summed yet)
+                    l *= keep;
+#pragma unroll
+                    for (int d = 0; d < D / 32; ++d) scale_product(o[d], keep);
+                }
+            }
+        };
+
+        // two tiles of keys and one of values into shared memory
+        find_pages(t0);
+        load_k(t0);
+        load_v(t0);
+        find_pages(t0 + 1);
+        store_scale(t0);
+        store_k(k_at);
+        clean_v(t0);
+        __syncthreads();
+        vs_next = s_scale[t0 & 3][tid & 3].y;
+        store_v(t0);
+        load_k(t0 + 1);
+        find_pages(t0 + 2);
+        store_scale(t0 + 1);
+        store_k(k_next);
+        __syncthreads();
+
+        // the first half's scores
+        each<D / 16>([&](auto S) {
+            const bf16x8_t k = *(const bf16x8_t*)(s_k + k_at + c * KROW + 16 * hi + 32 * S);
+            q[S].template to_vector<S == 0>(k, even);
+        });
+        product_done(even);
+        top = -inf32();
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) top = fmaxf(fmaxf(even[i], even[i + 1]), top);
+        read_scale(t0, 0);
+        use_scale();
+
+        // A step: one half's weights and sums, and the next one's scores, instruction by instruction.  Operand u of its products is
+        // read from shared memory AHEAD operands before its use, and behind every product comes the vector work that fits
+        // into its time (left to itself the compiler puts the products in one heap and the exponentials in another).
+        u32x4_t op[AHEAD + 1];
+        const uint8_t* lane_k = s_k + c * KROW + 16 * hi;
+        const uint8_t* lane_v = s_v[0] + c * VROW + 32 * hi;
+        auto fetch_k = [&](auto U, int at, int mt) { op[U % (AHEAD + 1)] = *(const u32x4_t*)(lane_k + at + 32 * mt * KROW + 32 * U); };
+        auto step = [&](auto MT, int tile, const f32x16_t& s, f32x16_t& next) {
+            constexpr int mt = MT, NP = (NQ + NV) / 2, E = 16;  // products, and weights of a lane
+            const uint8_t* from_v = lane_v + (tile & 1) * (D * VROW) + 64 * mt;
+            Weights<BF16> w[2];
+            float sum[2], p[2];
+            const float shift = bias - m;
+            top = -inf32();
+            // Weight x of the lane's 16 tokens; what is made of x - 2 and x - 1 comes with x, when they are there.
+            auto weight = [&](auto X) {
+                constexpr int x = X;
+                if constexpr (x % 2 == 0 && x > 0) {
+                    sum[0] = x == 2 ? p[0] : sum[0] + p[0];
+                    sum[1] = x == 2 ? p[1] : sum[1] + p[1];
+                    asm volatile("" : "+v"(sum[0]), "+v"(sum[1]));  // here and not later, with all of p's registers held for it
+                    w[(x - 2) / 8].put((x - 2) % 8, p[0], p[1]);
+                    if constexpr (x == E) l = fmaf(sum[0] + sum[1], back, l);
+                }
+                if constexpr (x < E) p[x & 1] = __builtin_amdgcn_exp2f(fmaf(s[x], cs, shift));
+            };
+            auto largest = [&](auto X) {
+                top = fmaxf(fmaxf(next[2 * X], next[2 * X + 1]), top);
+                asm volatile("" : "+v"(top));  // (the same)
+            };
+            each<NP>([&](auto F) {
+                constexpr int f = F, ahead = f + AHEAD;
+                if constexpr (ahead < NQ / 2) fetch_k(std::integral_constant<int, ahead>{}, mt ? k_next : k_at, 1 - mt);
+                else if constexpr (ahead < NP) {
+                    constexpr int d = (ahead - NQ / 2) % (D / 32), j = (ahead - NQ / 2) / (D / 32);
+                    op[ahead % (AHEAD + 1)] = *(const u32x4_t*)(from_v + 32 * d * VROW + 16 * j);
+                } else fetch_k(std::integral_constant<int, ahead - NP>{}, k_next, mt);  // the next step's
+                const u32x4_t x = op[f % (AHEAD + 1)];
+                if constexpr (f < NQ / 2) q[f].template to_vector<f == 0>(__builtin_bit_cast(bf16x8_t, x), next);
+                else {
+                    constexpr int d = (f - NQ / 2) % (D / 32), j = (f - NQ / 2) / (D / 32);
+                    o[d] = w[j].times(__builtin_bit_cast(typename Weights<BF16>::Codes, x), o[d]);
+                }
+                // the weights, all of them by the last quarter of the products, which is what the second half of them is for
+                constexpr int e0 = std::min(f * 4 * (E + 1) / (3 * NP), E + 1), e1 = std::min((f + 1) * 4 * (E + 1) / (3 * NP), E + 1);
+                each<e1 - e0>([&](auto I) { weight(std::integral_constant<int, e0 + I>{}); });
+                // the next half's largest scores, from a little after its last product on
+                constexpr int first = NP / 2 + (NP >= 16 ? 3 : 2), span = NP - first;
+                if constexpr (f == first && NP < 16) product_done(next);
+                if constexpr (f >= first) {
+                    constexpr int g0 = (f - first) * (E / 2) / span, g1 = (f - first + 1) * (E / 2) / span;
+                    each<g1 - g0>([&](auto I) { largest(std::integral_constant<int, g0 + I>{}); });
+                }
+                // the tiles to come: loaded in a tile's first step, stored at the end of its second (no step reads there before
+                // the barrier behind it)
+                if constexpr (mt == 0) {
+                    if constexpr (f == NP / 4) load_v(tile + 1);
+                    if constexpr (f == NP / 4 + 1) load_k(tile + 2);
+                    if constexpr (f == NP / 4 + 2) find_pages(tile + 3);
+                } else {
+                    if constexpr (f == 1) vs_next = s_scale[(tile + 1) & 3][tid & 3].y;
+                    if constexpr (f == NP - 4) clean_v(tile + 1);
+                    if constexpr (f == NP - 3) store_v(tile + 1);
+                    if constexpr (f == NP - 2) store_k(k_last);
+                }
+                if constexpr (f == NP / 2) read_scale(tile + mt, 1 - mt);
+                if constexpr (f == NP - 1) use_scale();
+                STEP();
+            });
+        };
+        each<AHEAD>([&](auto U) { fetch_k(U, k_at, 1); });
+        settle(std::true_type{}, t0, 0, even);
+        for (int tile = t0; tile < t1; ++tile) {
+            step(std::integral_constant<int, 0>{}, tile, even, odd);
+            settle(std::false_type{}, tile, 1, odd);
+            step(std::integral_constant<int, 1>{}, tile, odd, even);
+            store_scale(tile + 2);
+            const int k = k_at;
+            k_at = k_next;
+            k_next = k_last;
+            k_last = k;
+            __syncthreads();
+            if (tile + 1 < t1) settle(std::false_type{}, tile + 1, 0, even);
+        }
+
+        // the rows' answers, or what this piece of the item adds to them
+        const int own = fresh_lane(), col = own & 31, half = own >> 5;
+        const bool whole = t0 == 0 && t1 == it.tiles;
+        const int64_t slot = q8_slot(piece, t0 == 0) * BM + wave * 32 + col;
+        if (wave == 0 && own == 0 && sp.cut && t0 == 0) {  // (of several items that begin here only the last may be cut)
+            const int pieces = (int)div64(it.at + it.tiles - 1, share) - piece + 1, id = (b * a.c.H + h) * sp.row_blocks + rb;
+            sp.cut[sp.few ? id : piece] = make_int2(sp.few ? piece : id, pieces);
+        }
+        float sum = l + __shfl_xor(l, 32);
+        if (bad) sum = nan32();
+        const int r = rb * BM + wave * 32 + col, i = r / G, hq = h * G + r % G;
+        if (r < R) {
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int d4 = 32 * d + 8 * z + 4 * half;
+                    const f32x4_t x = {o[d][4 * z], o[d][4 * z + 1], o[d][4 * z + 2], o[d][4 * z + 3]};
+                    if (whole) q8_store_row<BF16>(a, b, i, hq, d4, m, sum, x);
+                    else *(f32x4_t*)(sp.part_o + slot * D + d4) = x;
+                }
+            if (!whole && half == 0) *(float2*)(sp.part_ml + slot * 2) = make_float2(m, sum);
+        }
+
+        // Rows that see a NaN value taken out above: which dims of which rows is the product of where the NaNs are
+        // with what the rows see.  What is NaN of what this thread has just stored becomes it.
+        if (__any(hidden_nan != 0)) s_nan = 1;
+        __syncthreads();
+        if (s_nan) {
+            const int sees_to = bad || r >= R ? 0 : min(len - a.n_q + i + 1, len);
+#pragma unroll 1
+            for (int t = max(t0, max(first_end, 0) / kTile); t < t1; ++t)
+#pragma unroll 1
+                for (int d = 0; d < D / 32; ++d) {
+                    f32x16_t hits;
+#pragma unroll
+                    for (int z = 0; z < 16; ++z) hits[z] = 0.f;
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        const int tok = t * kTile + 32 * mt + 16 * half;
+                        const int slot_of = min(tok >> logP, a.max_pages - 1), p = pages[slot_of];
+                        const int page = tok < len && p >= 0 && p < a.c.n_pages ? p : 0;
+                        u32x4_t is = *(const u32x4_t*)(a.c.v + (((int64_t)page * a.c.H + h) * D + 32 * d + col) * P + (tok & (P - 1)));
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) is[z] = nan_codes(is[z]) * 0x38u;  // the code of 1
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float f[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) f[z] = tok + 8 * j + z < sees_to ? 1.f : 0.f;
+                            Weights<BF16> sees;
+                            sees.set(f);
+                            hits = sees.times(Weights<BF16>::codes(is[2 * j], is[2 * j + 1]), hits);
+                        }
+                    }
+#pragma unroll
+                    for (int z = 0; z < 16; ++z) {
+                        if (!(hits[z] > 0.f)) continue;  // (rows past the last see nothing)
+                        const int dim = 32 * d + (z & 3) + 8 * (z >> 2) + 4 * half;
+                        if (!whole) sp.part_o[slot * D + dim] = nan32();
+                        else {
+                            const int64_t to = (int64_t)b * a.out.seq + (int64_t)hq * a.out.head + (int64_t)i * a.out.token + dim;
+                            if (BF16) ((uint16_t*)a.out.base)[to] = 0x7FC0;
+                            else ((float*)a.out.base)[to] = nan32();
+                        }
+                    }
+                }
+        }
+
+        at = it.at + t1;
+        __syncthreads();  // the next item's tiles come into the same memory
+    }
+}
+
+}  // namespace
+
+// More rows of a sequence and KV head than this take this kernel.
+constexpr int64_t kPromptRows = 64;
+
+Q8Plan q8_prompt_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus) {
+    Q8Plan p{};
+    const int64_t R = (int64_t)n_q * (Hq / H);
+    if (R <= kPromptRows) return p;
+    const bool bf16 = e == Elem::BF16;
+    p.prompt = true;
+    p.rows = bf16 && d == 128 && R > 128 ? 256 : 128;
+    p.row_blocks = (int)((R + p.rows - 1) / p.rows);
+    const int tiles = std::max(1, (max_len + kTile - 1) / kTile), per_cu = d == 64 ? 2 : 1;
+    p.grid = (int)std::min<double>((double)per_cu * cus, (double)B * H * p.row_blocks * tiles);
+    p.splits = p.grid > 1 && tiles > 1;
+    return p;
+}
+
+template <bool BF16, int D>
+static hipError_t launch(const Q8Attend& a, const Q8Pieces& sp, hipStream_t s) {
+    const dim3 grid((unsigned)sp.grid);
+    if (sp.rows == 128) hipLaunchKernelGGL((q8_prompt_kernel<BF16, D, 4>), grid, dim3(256), 0, s, a, sp);
+    else if constexpr (BF16 && D == 128) hipLaunchKernelGGL((q8_prompt_kernel<BF16, D, 8>), grid, dim3(512), 0, s, a, sp);
+    return hipGetLastError();
+}
+
+hipError_t launch_q8_prompt(Elem e, const Q8Attend& a, const Q8Pieces& sp, hipStream_t s) {
+    if (e == Elem::BF16) return a.c.d == 128 ? launch<true, 128>(a, sp, s) : launch<true, 64>(a, sp, s);
+    return a.c.d == 128 ? launch<false, 128>(a, sp, s) : launch<false, 64>(a, sp, s);
+}
+
+}  // namespace kvmap
