@@ -49,7 +49,7 @@ struct TileData {
 // spills of parts of matrix operands have given wrong sums (an fp32 instance of four row tiles), so fp32
 // stops at two row tiles and a test reads every instance's scratch size.
 template <bool BF16, int D, int NT>
-constexpr int kOccupancy = !BF16 ? (NT == 1 ? 2 : 1) : NT == 1 ? 3 : NT == 2 ? 2 : 1;
+constexpr int kOccupancy = BF16 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 2 : 1);
 
 // Sums of the lanes up to and including one's own.
 __device__ __forceinline__ uint32_t wave_scan(uint32_t x, int lane) {
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.Hq / a.c.H, R = a.n_q * G;
     const int P = a.c.page, logP = 31 - __clz(P);
-    const int items = a.c.H * sp.row_blocks;  // of one sequence
+    const int items = a.c.H;  // of one sequence
     const float y2 = a.scale * kLog2e;
 
     // this workgroup's piece [at, stop) of the line of steps, and the sequence that it begins in
@@ -139,9 +139,8 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
         }
         const bool bad = len < 0 || len > a.max_len;
         const int tiles = bad ? 0 : (len + kTile - 1) / kTile;
-        const int item = __builtin_amdgcn_readfirstlane((int)div64(at - base, steps));
-        const int h = item / sp.row_blocks, rb = item % sp.row_blocks;
-        const uint64_t item_at = base + (uint64_t)item * steps;
+        const int h = __builtin_amdgcn_readfirstlane((int)div64(at - base, steps));
+        const uint64_t item_at = base + (uint64_t)h * steps;
         const int s_begin = (int)(at - item_at), s_end = (int)min((uint64_t)steps, stop - item_at);
         int x0 = tid;
         asm volatile("" : "+v"(x0));  // keeps products of it with strides from being held across items: registers are full
@@ -151,10 +150,10 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
         // this lane's rows: their queries, and the tokens that they see
         Query<BF16> q[NT][D / 32];
         int end[NT];
-        const int first_end = len - a.n_q + rb * ROWS / G + 1;  // the fewest tokens that a row of the block sees
+        const int first_end = len - a.n_q + 1;  // the fewest tokens that a row sees
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = rb * ROWS + n * 16 + c;
+            const int r = n * 16 + c;
             const int i = r / G, hq = h * G + r % G;
             end[n] = len - a.n_q + i + 1;
 #pragma unroll
@@ -371,10 +370,10 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
             for (int d = 0; d < D / 16; ++d) *(f32x4_t*)&s_o[wave][n * 16 + c][16 * d + 4 * g] = o[n][d];
         }
         __syncthreads();
-        const int rows = min(ROWS, R - rb * ROWS);
+        const int rows = min(ROWS, R);
         asm volatile("" : "+v"(x0));  // (nor across the loop above)
         if (x0 == 0 && sp.cut && s_begin == 0) {  // (of several items that begin here only the last may be cut)
-            const int pieces = (int)div64(item_at + steps - 1, share) - (int)blockIdx.x + 1, id = b * items + item;
+            const int pieces = (int)div64(item_at + steps - 1, share) - (int)blockIdx.x + 1, id = b * items + h;
             sp.cut[sp.few ? id : (int)blockIdx.x] = make_int2(sp.few ? (int)blockIdx.x : id, pieces);
         }
         if (s_begin > 0 || s_end < steps) {
@@ -394,8 +393,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
                 f32x4_t sum;
                 join_waves<ROWS, LDO>(s_o, s_ml, row, d4, top, lsum, sum);
                 if (bad) lsum = nan32();
-                const int r = rb * ROWS + row;
-                q8_store_row<BF16>(a, b, r / G, h * G + r % G, d4, top, lsum, sum);
+                q8_store_row<BF16>(a, b, row / G, h * G + row % G, d4, top, lsum, sum);
             }
         }
         at = item_at + s_end;
@@ -403,11 +401,8 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
     }
 }
 
-// Row tiles of a workgroup: as many as the rows fill and the registers hold.
-int row_tiles(int64_t R, bool bf16, int d) { return R <= 16 ? 1 : R <= 32 || !bf16 || d > 64 ? 2 : 4; }
-
 // Workgroups that a CU holds at once, as the registers (kOccupancy) and the shared memory allow.
-constexpr int per_cu(bool bf16, int nt) { return bf16 ? (nt == 1 ? 3 : nt == 2 ? 2 : 1) : (nt == 1 ? 2 : 1); }
+constexpr int per_cu(bool bf16, int nt) { return bf16 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 2 : 1); }
 
 }  // namespace
 
@@ -415,11 +410,11 @@ Q8Plan q8_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len,
     Q8Plan p = q8_prompt_plan(e, B, n_q, Hq, H, d, max_len, cus);
     if (p.rows) return p;
     const int64_t R = (int64_t)n_q * (Hq / H);
-    const int nt = row_tiles(R, e == Elem::BF16, d);
+    const int nt = R <= 16 ? 1 : 2;  // 16-row tiles of a workgroup (q8_prompt.hip takes more than 32 rows)
     p.rows = 16 * nt;
-    p.row_blocks = (int)((R + p.rows - 1) / p.rows);
+    p.row_blocks = 1;
     // a workgroup for every step that the lengths can bring, up to what the chip holds at once
-    const double steps = (double)B * H * p.row_blocks * q8_steps(max_len, max_len);
+    const double steps = (double)B * H * q8_steps(max_len, max_len);
     p.grid = (int)std::min<double>((double)per_cu(e == Elem::BF16, nt) * cus, steps);
     p.splits = p.grid > 1 && q8_steps(max_len, max_len) > 1;  // (items of one step are never cut)
     return p;
@@ -434,8 +429,7 @@ template <bool BF16, int D>
 static hipError_t launch_decode(const Q8Attend& a, const Q8Pieces& sp, hipStream_t s) {
     const dim3 grid((unsigned)sp.grid);
     if (sp.rows == 16) hipLaunchKernelGGL((q8_decode_kernel<BF16, D, 1>), grid, dim3(256), 0, s, a, sp);
-    else if (sp.rows == 32) hipLaunchKernelGGL((q8_decode_kernel<BF16, D, 2>), grid, dim3(256), 0, s, a, sp);
-    else if constexpr (BF16 && D == 64) hipLaunchKernelGGL((q8_decode_kernel<BF16, D, 4>), grid, dim3(256), 0, s, a, sp);
+    else hipLaunchKernelGGL((q8_decode_kernel<BF16, D, 2>), grid, dim3(256), 0, s, a, sp);
     return hipGetLastError();
 }
 

@@ -176,7 +176,10 @@ __device__ __forceinline__ uint64_t div64(uint64_t a, uint64_t b) {
 // A piece's slots: one for an item that it begins (its last), one for an item that began before (its first).
 __host__ __device__ __forceinline__ int64_t q8_slot(int64_t piece, bool begins) { return 2 * piece + begins; }
 
-// 4 dims of one answered row, and at dim 0 its lse; a row whose weights sum to 0 saw no token.
+// A row's lse; one whose weights sum to 0 saw no token.
+__device__ __forceinline__ float q8_lse(float top, float lsum) { return lsum == 0.f ? -inf32() : (top + __builtin_amdgcn_logf(lsum)) * kLn2; }
+
+// 4 dims of one answered row, and at dim 0 its lse.
 template <bool BF16>
 __device__ __forceinline__ void q8_store_row(const Q8Attend& a, int b, int i, int hq, int d4, float top, float lsum, f32x4_t sum) {
     sum *= lsum == 0.f ? 0.f : 1.f / lsum;
@@ -186,7 +189,7 @@ __device__ __forceinline__ void q8_store_row(const Q8Attend& a, int b, int i, in
     else
         *(f32x4_t*)((float*)a.out.base + at) = sum;
     if (d4 == 0 && a.lse)
-        a.lse[((int64_t)b * a.n_q + i) * a.Hq + hq] = lsum == 0.f ? -inf32() : (top + __builtin_amdgcn_logf(lsum)) * kLn2;
+        a.lse[((int64_t)b * a.n_q + i) * a.Hq + hq] = q8_lse(top, lsum);
 }
 
 }  // namespace

@@ -50,6 +50,11 @@ __device__ __forceinline__ int block_tiles(const Q8Attend& a, int G, int len, in
     const int end = block_end(a, G, len, rb, bm);
     return end < 1 ? 1 : (end - 1) / kTile + 1;
 }
+// An item costs as much as its tiles and kItemCost more: page table, queries, first tiles, answers.  (Counted as its tiles
+// alone, 333 queries of 3 heads in 4 sequences, one of them empty, took 209 us instead of 73.)
+template <bool BF16>
+constexpr int kItemCost = BF16 ? 5 : 2;
+
 __device__ __forceinline__ uint64_t wave_scan(uint64_t x, int lane) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -59,9 +64,9 @@ __device__ __forceinline__ uint64_t wave_scan(uint64_t x, int lane) {
     return x;
 }
 __device__ __forceinline__ uint64_t last_lane(uint64_t x) { return __shfl((unsigned long long)x, 63); }
-// Tiles of all row blocks of one head: of sequence b0 + lane (0 past the last), lanes going over the sequences or over the row
+// Cost of all row blocks of one head: of sequence b0 + lane (0 past the last), lanes going over the sequences or over the row
 // blocks, whichever is fewer rounds.
-__device__ __forceinline__ uint64_t head_tiles(const Q8Attend& a, int G, int b0, int row_blocks, int bm, int lane) {
+__device__ __forceinline__ uint64_t head_cost(const Q8Attend& a, int G, int b0, int row_blocks, int bm, int extra, int lane) {
     uint64_t sum = 0;
     const int n = min(a.B - b0, 64);
     if (n * ((row_blocks + 63) / 64) < row_blocks) {
@@ -69,61 +74,62 @@ __device__ __forceinline__ uint64_t head_tiles(const Q8Attend& a, int G, int b0,
             const int len = a.len[b0 + i];
             uint64_t s = 0;
             for (int r0 = 0; r0 < row_blocks; r0 += 64)
-                s += last_lane(wave_scan(r0 + lane < row_blocks ? block_tiles(a, G, len, r0 + lane, bm) : 0, lane));
+                s += last_lane(wave_scan(r0 + lane < row_blocks ? block_tiles(a, G, len, r0 + lane, bm) + extra : 0, lane));
             if (i == lane) sum = s;
         }
     } else if (lane < n) {
         const int len = a.len[b0 + lane];
-        for (int rb = 0; rb < row_blocks; ++rb) sum += block_tiles(a, G, len, rb, bm);
+        for (int rb = 0; rb < row_blocks; ++rb) sum += block_tiles(a, G, len, rb, bm) + extra;
     }
     return sum;
 }
 
 // An item, and where it lies in the line.
 struct Item {
-    int b, h, rb, tiles;
+    int b, h, rb, cost;
     uint64_t at;
 };
-// The line's length, and the item that holds its tile u (u < the length): every lane of the wave alike.
-__device__ __forceinline__ uint64_t line_length(const Q8Attend& a, int G, int row_blocks, int bm, int lane) {
-    uint64_t total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) total += last_lane(wave_scan(head_tiles(a, G, b0, row_blocks, bm, lane), lane));
+// The line's length; `first` is what head_cost gives for the first 64 sequences.  Every lane of the wave alike.
+__device__ __forceinline__ uint64_t line_length(const Q8Attend& a, int G, int row_blocks, int bm, int extra, int lane, uint64_t first) {
+    uint64_t total = last_lane(wave_scan(first, lane));
+    for (int b0 = 64; b0 < a.B; b0 += 64) total += last_lane(wave_scan(head_cost(a, G, b0, row_blocks, bm, extra, lane), lane));
     return total * a.c.H;
 }
-__device__ __forceinline__ bool find_item(const Q8Attend& a, int G, int row_blocks, int bm, int lane, uint64_t u, Item& it) {
-    uint64_t base = 0, head = 0;
-    for (int b0 = 0;; b0 += 64) {
-        if (b0 >= a.B) return false;  // (not reached while the lengths stay as they were summed)
-        const uint64_t mine = head_tiles(a, G, b0, row_blocks, bm, lane);
+// The item that holds the line's unit u (less than its length).
+__device__ __forceinline__ Item find_item(const Q8Attend& a, int G, int row_blocks, int bm, int extra, int lane, uint64_t first, uint64_t u) {
+    Item it;
+    uint64_t base = 0, mine = first;
+    int b0 = 0;
+    while (true) {
         const uint64_t upto = wave_scan(mine, lane) * a.c.H;
         const uint64_t past = __ballot(base + upto > u);
-        if (past) {
-            const int n = __ffsll((unsigned long long)past) - 1;
-            it.b = b0 + n;
-            head = __shfl((unsigned long long)mine, n);
-            base += __shfl((unsigned long long)upto, n) - head * a.c.H;
+        const int n = past ? __ffsll((unsigned long long)past) - 1 : 63;
+        it.b = min(b0 + n, a.B - 1);  // (past is not 0 in the end, while the lengths stay as they were summed)
+        if (past || b0 + 64 >= a.B) {
+            mine = __shfl((unsigned long long)mine, n);
+            base += __shfl((unsigned long long)upto, n) - mine * a.c.H;
             break;
         }
         base += last_lane(upto);
+        b0 += 64;
+        mine = head_cost(a, G, b0, row_blocks, bm, extra, lane);
     }
-    it.h = (int)div64(u - base, head);
-    base += (uint64_t)it.h * head;
+    it.h = min((int)div64(u - base, max(mine, (uint64_t)1)), a.c.H - 1);
+    base += (uint64_t)it.h * mine;
     const int len = a.len[it.b];
     for (int r0 = 0;; r0 += 64) {
-        if (r0 >= row_blocks) return false;  // (as above)
-        const uint64_t mine = r0 + lane < row_blocks ? block_tiles(a, G, len, r0 + lane, bm) : 0;
-        const uint64_t upto = wave_scan(mine, lane);
+        const uint64_t cost = r0 + lane < row_blocks ? block_tiles(a, G, len, r0 + lane, bm) + extra : 0;
+        const uint64_t upto = wave_scan(cost, lane);
         const uint64_t past = __ballot(base + upto > u);
-        if (past) {
-            const int n = __ffsll((unsigned long long)past) - 1;
+        if (past || r0 + 64 >= row_blocks) {
+            const int n = past ? __ffsll((unsigned long long)past) - 1 : row_blocks - 1 - r0;
             it.rb = r0 + n;
-            it.tiles = (int)__shfl((unsigned long long)mine, n);
-            it.at = base + __shfl((unsigned long long)upto, n) - it.tiles;
-            break;
+            it.cost = (int)__shfl((unsigned long long)cost, n);
+            it.at = base + __shfl((unsigned long long)upto, n) - it.cost;
+            return it;
         }
         base += last_lane(upto);
     }
-    return true;
 }
 
 // The lane, computed where it is wanted: registers are full, and the compiler would hold it, and its products with strides,
@@ -132,6 +138,13 @@ __device__ __forceinline__ int fresh_lane() {
     int lane;
     asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(lane));
     return lane;
+}
+
+// What the wave's lanes have written to shared memory is there for its other lanes.
+__device__ __forceinline__ void wave_memory() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 template <bool BF16, int D, int WAVES>
@@ -145,8 +158,8 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
     constexpr int NQ = D / 8, NV = D / 8;      // operands of a tile: keys, values
     constexpr int AHEAD = 3;
     constexpr int CPT = D / 16;                // such loads of a token's keys
-    __shared__ __align__(16) uint8_t s_k[3 * KBYTES];
-    __shared__ __align__(16) uint8_t s_v[2][D * VROW];
+    __shared__ __align__(16) uint8_t s_k[3 * KBYTES + 2 * D * VROW];
+    uint8_t* const s_v = s_k + 3 * KBYTES;
     __shared__ int s_nan;                      // some value was taken out
     __shared__ float2 s_scale[4][4];           // k_scale, v_scale of 16 tokens each; a tile's are written with its keys
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -156,45 +169,40 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
 
     // this workgroup's piece; those of one XCD (workgroups 8 apart) are neighbours, which share a head's keys and values
     const int piece = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
-    const uint64_t total = line_length(a, G, sp.row_blocks, BM, fresh_lane());
-    const uint64_t share = div64(total + sp.grid - 1, sp.grid);
-    uint64_t at = share * piece;
-    const uint64_t stop = at + share < total ? at + share : total;
+    constexpr int COST = kItemCost<BF16>;
+    const uint64_t first = head_cost(a, G, 0, sp.row_blocks, BM, COST, fresh_lane());
+    const uint64_t total = line_length(a, G, sp.row_blocks, BM, COST, fresh_lane(), first);
+    const uint64_t share = div64(total + sp.grid - 1, sp.grid), at = share * piece, stop = at + share < total ? at + share : total;
     if (threadIdx.x == 0 && sp.cut && !sp.few) sp.cut[piece] = make_int2(0, 1);
 
-    while (at < stop) {
-        Item it;
-        if (!find_item(a, G, sp.row_blocks, BM, fresh_lane(), at, it)) return;
+    if (at >= stop) return;
+    Item it = find_item(a, G, sp.row_blocks, BM, COST, fresh_lane(), first, at);
+    bool again = false;
+    for (; it.at < stop; it.at += it.cost, ++it.rb) {
+        if (it.rb == sp.row_blocks) {
+            it.rb = 0;
+            if (++it.h == a.c.H) {
+                it.h = 0;
+                if (++it.b == a.B) return;  // (not reached while the lengths stay as they were summed)
+            }
+        }
         const int b = __builtin_amdgcn_readfirstlane(it.b), h = __builtin_amdgcn_readfirstlane(it.h);
         const int rb = __builtin_amdgcn_readfirstlane(it.rb);
-        const int len = a.len[b];
+        const int len = a.len[b], tiles = block_tiles(a, G, len, rb, BM);
+        it.cost = tiles + COST;
+        const Q8Cut cut = q8_cut(it.at + COST, tiles, share, piece);
+        const int t0 = __builtin_amdgcn_readfirstlane(cut.t0), t1 = __builtin_amdgcn_readfirstlane(cut.t1);
+        if (t0 >= t1) continue;
+        if (again) __syncthreads();  // this item's tiles come into the memory of the one before
+        again = true;
         const bool bad = len < 0 || len > a.max_len;
-        const int t0 = __builtin_amdgcn_readfirstlane((int)(at - it.at));
-        const int t1 = __builtin_amdgcn_readfirstlane((int)min((uint64_t)it.tiles, stop - it.at));
         const int first_end = bad ? 0 : len - a.n_q + rb * BM / G + 1;               // the fewest tokens that a row sees
         const int wave_end = bad ? 0 : len - a.n_q + (rb * BM + wave * 32) / G + 1;  // the same of the wave's rows
         const int32_t* pages = a.pages + (int64_t)b * a.max_pages;
 
         const int tid = 64 * wave + fresh_lane(), c = tid & 31, hi = tid >> 5 & 1;
-        Query<BF16> q[D / 16];
         const int row = rb * BM + wave * 32 + c;  // of the sequence and head
         const int end = bad ? 0 : min(len - a.n_q + row / G + 1, len);
-#pragma unroll
-        for (int st = 0; st < D / 16; ++st) {
-            if (row < R)
-                q[st].load(a.q.base, (int64_t)b * a.q.seq + (int64_t)(h * G + row % G) * a.q.head + (int64_t)(row / G) * a.q.token + 16 * st + 8 * hi);
-            else
-                q[st].zero();
-            q[st].keep();
-        }
-        f32x16_t o[D / 32];
-        float m = kNone, l = 0.f;
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-            keep_accumulated(o[d]);
-        }
 
         // A thread's part of a tile: keys as 16 dims of the tokens ktok(j), values as 16 tokens (group tid & 3) of the dims
         // vdim(j), and the group's scales.
@@ -209,7 +217,7 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
         const float *ksh = a.c.ks + h, *vsh = a.c.vs + h;
         const uint32_t page_bytes = a.c.H * P * D;  // of all heads (H < 2^16)
         u32x4_t kx[NC], vx[NC];
-        int pk[NC], pg, pv, ps;
+        int pk[NC], pg, pv;
         float2 sc;
         auto find_pages = [&](int tile) {
 #pragma unroll
@@ -228,14 +236,13 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
             pv = page_of(tile * kTile + 16 * (tid & 3), pg);
             const uint64_t g = (uint64_t)(uint32_t)max(pv, 0) * (uint32_t)a.c.H;
             sc = make_float2(ksh[g], vsh[g]);
-            ps = pv;
         };
         auto load_v = [&](int tile) {
             const uint8_t* v = vh + ((tile * kTile) & (P - 1)) + ((uint64_t)(uint32_t)max(pv, 0) * page_bytes + voff);
 #pragma unroll
             for (int j = 0; j < NC; ++j) vx[j] = *(const u32x4_t*)(v + THREADS / 4 * j * P);
         };
-        auto store_k = [&](int at) {
+        auto store_k = [&](int at, const u32x4_t (&kx)[NC]) {
             uint8_t* to = s_k + at;
 #pragma unroll
             for (int j = 0; j < NC; ++j) {
@@ -245,10 +252,12 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
                 w[1] = bf16_codes(kx[j][2], kx[j][3]);
             }
         };
-        auto store_scale = [&](int tile) {
-            // a page out of range makes the scores that need it NaN; past the sequence's end there is no page
-            if (tid < 4) s_scale[tile & 3][tid] = ps < 0 || tile * kTile + 16 * tid >= len ? make_float2(nan32(), 1.f) : sc;
+        // A page out of range makes the scores that need it NaN; past the sequence's end there is no page.
+        auto store_scale = [&](int tile, float2 sc, int pv) {
+            if (tid < 4) s_scale[tile & 3][tid] = pv < 0 || tile * kTile + 16 * tid >= len ? make_float2(nan32(), 1.f) : sc;
         };
+        float vs_next;  // the scale of the values that are stored next
+        auto hold_scale = [&](int tile, float2 sc, int pv) { vs_next = pv < 0 || tile * kTile + 16 * (tid & 3) >= len ? 1.f : sc.y; };
         uint32_t hidden_nan = 0;
         if (tid == 0) s_nan = 0;
         auto clean_v = [&](int tile) {
@@ -269,9 +278,8 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
                 }
             }
         };
-        float vs_next;  // the scale of the values that this stores
         auto store_v = [&](int tile) {
-            uint8_t* to = s_v[tile & 1];
+            uint8_t* to = s_v + (tile & 1) * (D * VROW);
             const int ev = (int)(__float_as_uint(vs_next) >> 23) - 127;
             const float small = ev < -90 ? vs_next * 0x1p90f : 1.f;  // (see bias below)
 #pragma unroll
@@ -296,6 +304,54 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
             bias = (float)max(ev, -90);  // (values under 2^-82: l would overflow on their 1 / v_scale)
             back = __uint_as_float((uint32_t)(127 - max(ev, -90)) << 23);  // 1 / v_scale
         };
+        // Two tiles of keys and one of values into shared memory.  All loads first: they wait for one another only through the
+        // page table.
+        Query<BF16> q[D / 16];
+        f32x16_t o[D / 32];
+        float m = kNone, l = 0.f;
+        {
+            int pk1[NC];
+#pragma unroll
+            for (int j = 0; j < NC; ++j) pk1[j] = entry_of((t0 + 1) * kTile + wave_tok(j));
+            const int pg1 = entry_of((t0 + 1) * kTile + 16 * (tid & 3));
+            find_pages(t0);
+            load_k(t0);
+            load_v(t0);
+            u32x4_t k0[NC];
+            const float2 sc0 = sc;
+            const int pv0 = pv;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                k0[j] = kx[j];
+                pk[j] = pk1[j];
+            }
+            pg = pg1;
+            load_k(t0 + 1);
+            find_pages(t0 + 2);
+            const int64_t q_at = (int64_t)b * a.q.seq + (int64_t)(h * G + row % G) * a.q.head + (int64_t)(row / G) * a.q.token + 8 * hi;
+#pragma unroll
+            for (int st = 0; st < D / 16; ++st) {
+                if (row < R) q[st].load(a.q.base, q_at + 16 * st);
+                else q[st].zero();
+            }
+            store_scale(t0, sc0, pv0);
+            store_scale(t0 + 1, sc, pv);
+            hold_scale(t0, sc0, pv0);
+            store_k(k_at, k0);
+            clean_v(t0);
+            store_v(t0);
+            store_k(k_next, kx);
+#pragma unroll
+            for (int st = 0; st < D / 16; ++st) q[st].keep();
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+                keep_accumulated(o[d]);
+            }
+        }
+        __syncthreads();
+
         // The mask, where some row of the wave does not see all of the half; and the maximum moved where a score passes it by more
         // than kSlack.
         auto settle = [&](auto FIRST, int tile, int mt, f32x16_t& x) {
@@ -324,23 +380,6 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
             }
         };
 
-        // two tiles of keys and one of values into shared memory
-        find_pages(t0);
-        load_k(t0);
-        load_v(t0);
-        find_pages(t0 + 1);
-        store_scale(t0);
-        store_k(k_at);
-        clean_v(t0);
-        __syncthreads();
-        vs_next = s_scale[t0 & 3][tid & 3].y;
-        store_v(t0);
-        load_k(t0 + 1);
-        find_pages(t0 + 2);
-        store_scale(t0 + 1);
-        store_k(k_next);
-        __syncthreads();
-
         // the first half's scores
         each<D / 16>([&](auto S) {
             const bf16x8_t k = *(const bf16x8_t*)(s_k + k_at + c * KROW + 16 * hi + 32 * S);
@@ -358,7 +397,7 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
         // into its time (left to itself the compiler puts the products in one heap and the exponentials in another).
         u32x4_t op[AHEAD + 1];
         const uint8_t* lane_k = s_k + c * KROW + 16 * hi;
-        const uint8_t* lane_v = s_v[0] + c * VROW + 32 * hi;
+        const uint8_t* lane_v = s_v + c * VROW + 32 * hi;
         auto fetch_k = [&](auto U, int at, int mt) { op[U % (AHEAD + 1)] = *(const u32x4_t*)(lane_k + at + 32 * mt * KROW + 32 * U); };
         auto step = [&](auto MT, int tile, const f32x16_t& s, f32x16_t& next) {
             constexpr int mt = MT, NP = (NQ + NV) / 2, E = 16;  // products, and weights of a lane
@@ -410,13 +449,15 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
                 // the barrier behind it)
                 if constexpr (mt == 0) {
                     if constexpr (f == NP / 4) load_v(tile + 1);
-                    if constexpr (f == NP / 4 + 1) load_k(tile + 2);
+                    if constexpr (f == NP / 4 + 1) {
+                        hold_scale(tile + 1, sc, pv);
+                        load_k(tile + 2);
+                    }
                     if constexpr (f == NP / 4 + 2) find_pages(tile + 3);
                 } else {
-                    if constexpr (f == 1) vs_next = s_scale[(tile + 1) & 3][tid & 3].y;
                     if constexpr (f == NP - 4) clean_v(tile + 1);
                     if constexpr (f == NP - 3) store_v(tile + 1);
-                    if constexpr (f == NP - 2) store_k(k_last);
+                    if constexpr (f == NP - 2) store_k(k_last, kx);
                 }
                 if constexpr (f == NP / 2) read_scale(tile + mt, 1 - mt);
                 if constexpr (f == NP - 1) use_scale();
@@ -429,7 +470,7 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
             step(std::integral_constant<int, 0>{}, tile, even, odd);
             settle(std::false_type{}, tile, 1, odd);
             step(std::integral_constant<int, 1>{}, tile, odd, even);
-            store_scale(tile + 2);
+            store_scale(tile + 2, sc, pv);
             const int k = k_at;
             k_at = k_next;
             k_next = k_last;
@@ -440,26 +481,60 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
 
         // the rows' answers, or what this piece of the item adds to them
         const int own = fresh_lane(), col = own & 31, half = own >> 5;
-        const bool whole = t0 == 0 && t1 == it.tiles;
+        const bool whole = t0 == 0 && t1 == tiles;
         const int64_t slot = q8_slot(piece, t0 == 0) * BM + wave * 32 + col;
         if (wave == 0 && own == 0 && sp.cut && t0 == 0) {  // (of several items that begin here only the last may be cut)
-            const int pieces = (int)div64(it.at + it.tiles - 1, share) - piece + 1, id = (b * a.c.H + h) * sp.row_blocks + rb;
-            sp.cut[sp.few ? id : piece] = make_int2(sp.few ? piece : id, pieces);
+            const int id = (b * a.c.H + h) * sp.row_blocks + rb;
+            sp.cut[sp.few ? id : piece] = make_int2(sp.few ? piece : id, cut.pieces);
         }
         float sum = l + __shfl_xor(l, 32);
         if (bad) sum = nan32();
         const int r = rb * BM + wave * 32 + col, i = r / G, hq = h * G + r % G;
-        if (r < R) {
+        if (r < R && half == 0) {
+            if (!whole) *(float2*)(sp.part_ml + slot * 2) = make_float2(m, sum);
+            else if (a.lse) a.lse[((int64_t)b * a.n_q + i) * a.Hq + hq] = q8_lse(m, sum);
+        }
+        // A lane holds 4 dims here and 4 there of one row; turned in the wave's part of shared memory, 64 dims at a time, rows leave
+        // in whole pieces (as the lanes hold them, 16 bytes a row and store, they took 9,000 cycles).
+        {
+            constexpr int LD = 64 + 4, DIMS = BF16 ? 8 : 4;  // floats of a row; dims of a lane's store
+            static_assert(WAVES * 32 * LD * 4 <= sizeof(s_k), "the waves' parts");
+            float* mine = (float*)s_k + wave * (32 * LD);
+            const float scale = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-            for (int d = 0; d < D / 32; ++d)
+            for (int p = 0; p < D / 64; ++p) {
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int d4 = 32 * d + 8 * z + 4 * half;
-                    const f32x4_t x = {o[d][4 * z], o[d][4 * z + 1], o[d][4 * z + 2], o[d][4 * z + 3]};
-                    if (whole) q8_store_row<BF16>(a, b, i, hq, d4, m, sum, x);
-                    else *(f32x4_t*)(sp.part_o + slot * D + d4) = x;
+                for (int d = 0; d < 2; ++d)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const f32x16_t& x = o[2 * p + d];
+                        *(f32x4_t*)(mine + col * LD + 32 * d + 8 * z + 4 * half) =
+                            f32x4_t{x[4 * z] * scale, x[4 * z + 1] * scale, x[4 * z + 2] * scale, x[4 * z + 3] * scale};
+                    }
+                wave_memory();
+                if (whole) {
+#pragma unroll
+                    for (int k = 0; k < 32 * 64 / (64 * DIMS); ++k) {
+                        const int y = (k * 64 + own) / (64 / DIMS), at = own % (64 / DIMS) * DIMS, ry = rb * BM + wave * 32 + y;
+                        if (ry >= R) continue;
+                        const int64_t to = (int64_t)b * a.out.seq + (int64_t)(h * G + ry % G) * a.out.head + (int64_t)(ry / G) * a.out.token + 64 * p + at;
+                        const f32x4_t x0 = *(const f32x4_t*)(mine + y * LD + at);
+                        if (BF16) {
+                            const f32x4_t x1 = *(const f32x4_t*)(mine + y * LD + at + 4);
+                            *(uint4*)((uint16_t*)a.out.base + to) = make_uint4(pack_bf16(x0[0], x0[1]), pack_bf16(x0[2], x0[3]), pack_bf16(x1[0], x1[1]), pack_bf16(x1[2], x1[3]));
+                        } else
+                            *(f32x4_t*)((float*)a.out.base + to) = x0;
+                    }
+                } else {
+                    float* to = sp.part_o + (slot - col) * D + 64 * p;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int y = k * 4 + own / 16, at = own % 16 * 4;
+                        if (rb * BM + wave * 32 + y < R) *(f32x4_t*)(to + y * D + at) = *(const f32x4_t*)(mine + y * LD + at);
+                    }
                 }
-            if (!whole && half == 0) *(float2*)(sp.part_ml + slot * 2) = make_float2(m, sum);
+                wave_memory();
+            }
         }
 
         // Rows that see a NaN value taken out above: which dims of which rows is the product of where the NaNs are
@@ -506,16 +581,14 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
                     }
                 }
         }
-
-        at = it.at + t1;
-        __syncthreads();  // the next item's tiles come into the same memory
     }
 }
 
 }  // namespace
 
-// More rows of a sequence and KV head than this take this kernel.
-constexpr int64_t kPromptRows = 64;
+// More rows of a sequence and KV head than this take this kernel.  (40, 48 and 64 rows of 16 sequences of up to 3,000 tokens:
+// 36.9, 62 (fp32, 8 heads) and 37.6 us here, 38.5, 79 and 42 in q8_attend.hip's; 24 and 32 rows: 35 here, 27 and 28 there.)
+constexpr int64_t kPromptRows = 32;
 
 Q8Plan q8_prompt_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus) {
     Q8Plan p{};

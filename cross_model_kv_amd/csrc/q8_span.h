@@ -44,6 +44,21 @@ KVMAP_HD Q8Span q8_span(int64_t start, int64_t count, int64_t n, int64_t j, cons
     return s;
 }
 
+// What piece w of a line of work, cut every `share` units, takes of an item whose tiles are the units at .. at + tiles: the
+// tiles [t0, t1), and where t0 is 0, the number of pieces that the item is in.
+struct Q8Cut {
+    int t0, t1, pieces;
+};
+KVMAP_HD int q8_cut_at(uint64_t u, uint64_t at, int tiles) { return u <= at ? 0 : u >= at + tiles ? tiles : (int)(u - at); }
+KVMAP_HD Q8Cut q8_cut(uint64_t at, int tiles, uint64_t share, uint64_t w) {
+    Q8Cut c;
+    c.t0 = q8_cut_at(w * share, at, tiles);
+    c.t1 = q8_cut_at((w + 1) * share, at, tiles);
+    c.pieces = 1;
+    if (c.t0 == 0 && c.t1 > 0 && c.t1 < tiles) c.pieces += (int)((at + tiles - 1) / share - at / share);
+    return c;
+}
+
 // Attention's steps over a sequence: at least one, also of an empty one and one whose length is out of range,
 // so that its rows are answered.
 constexpr int kQ8Step = 256;
