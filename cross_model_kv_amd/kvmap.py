@@ -282,18 +282,24 @@ def ridge_solve_host(mean_x, mean_y, M_xx, M_xy, lam: float, n_threads: int = 0)
 # device side (torch tensors for memory, torch streams)
 # ---------------------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
+    torch, dtype = _torch(), t.dtype
+    if dtype is torch.bfloat16:
         return BF16
-    if t.dtype == torch.float32:
+    if dtype is torch.float32:
         return F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    raise TypeError(f"unsupported dtype {dtype}")
 
 
 def _dev_ptr(t, name):
@@ -308,6 +314,14 @@ def _stream_handle(stream, device):
     torch = _torch()
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _stream_of(stream, index):
+    """The handle of `stream`, or of device `index`'s current stream, as an integer.  (Asked for without making a
+    Stream object, which takes longer than the rest of a small call's arguments.)"""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(index)
 
 
 def _chain(first, rest):
@@ -365,6 +379,7 @@ class Q8Cache:
         self.c = Q8CacheC(L, n_pages, H, page, d, _dev_ptr(k, "k"), _dev_ptr(v, "v"), _dev_ptr(k_scale, "k_scale"),
                           _dev_ptr(v_scale, "v_scale"))
         self.ref = ctypes.byref(self.c)
+        self.index = k.device.index
 
 
 class Context:
@@ -375,6 +390,9 @@ class Context:
         h = ctypes.c_void_p()
         _check(lib().kvmap_create(ctypes.byref(h), self.device), "kvmap_create")
         self._h = h
+        # the 8-bit cache calls' arguments
+        self._seqs, self._rows = Q8SeqsC(), (Q8RowsC(), Q8RowsC())
+        self._seqs_ref, self._rows_ref = ctypes.byref(self._seqs), tuple(ctypes.byref(r) for r in self._rows)
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
@@ -485,13 +503,14 @@ class Context:
         scales = lambda: torch.zeros((L, n_pages, H), dtype=torch.float32, device=dev)
         return Q8Cache(codes(L, n_pages, H, page, d), codes(L, n_pages, H, d, page), scales(), scales())
 
+    # A decode step makes these calls once a layer on a few rows, so their host time counts: no objects are made that
+    # the call does not need, and the argument structs belong to the context (which one thread uses at a time).
     def _q8_ints(self, t, name, shape):
-        torch = _torch()
-        if t.dtype != torch.int32 or t.shape != shape:
+        if t.dtype is not _torch_module.int32 or t.shape != shape:
             raise ValueError(f"{name} must be int32 {list(shape)}")
         return _dev_ptr(t, name)
 
-    def _q8_rows(self, name, cache, k, v, pages, start, n, count, layer, dtype, stream):
+    def _q8_rows(self, call, cache, k, v, pages, start, n, count, layer, dtype, stream):
         B, max_pages = pages.shape
         L = k.shape[0]
         shape = (L, B, cache.H, n, cache.d)
@@ -499,17 +518,19 @@ class Context:
             raise ValueError(f"k and v must be {list(shape)} ([layers][B][H][n][d], or [B][H][n][d] of one layer)")
         if not (k.is_cuda and v.is_cuda):
             raise ValueError("k and v must be device tensors")
-        ks, vs = k.stride(), v.stride()
-        if ks[4] != 1 or vs[4] != 1:
+        seqs, rk, rv = self._seqs, self._rows[0], self._rows[1]
+        rk.layer_stride, rk.seq_stride, rk.head_stride, rk.token_stride, k_last = k.stride()
+        rv.layer_stride, rv.seq_stride, rv.head_stride, rv.token_stride, v_last = v.stride()
+        if k_last != 1 or v_last != 1:
             raise ValueError("the head dim of k and v must be contiguous")
-        seqs = Q8SeqsC(B, max_pages, self._q8_ints(pages, "pages", (B, max_pages)), self._q8_ints(start, "start", (B,)),
-                       None if count is None else self._q8_ints(count, "count", (B,)))
-        st = getattr(lib(), name)(self._h, cache.ref, layer, L, ctypes.byref(seqs), n, dtype,
-                                  ctypes.byref(Q8RowsC(k.data_ptr(), ks[0], ks[1], ks[2], ks[3])),
-                                  ctypes.byref(Q8RowsC(v.data_ptr(), vs[0], vs[1], vs[2], vs[3])),
-                                  _stream_handle(stream, cache.k.device))
+        rk.base, rv.base = k.data_ptr(), v.data_ptr()
+        seqs.B, seqs.max_pages = B, max_pages
+        seqs.pages, seqs.start = self._q8_ints(pages, "pages", (B, max_pages)), self._q8_ints(start, "start", (B,))
+        seqs.count = None if count is None else self._q8_ints(count, "count", (B,))
+        st = call(self._h, cache.ref, layer, L, self._seqs_ref, n, dtype, self._rows_ref[0], self._rows_ref[1],
+                  _stream_of(stream, cache.index))
         if st:
-            _check(st, name)
+            _check(st, call.__name__)
 
     def q8_write(self, cache: Q8Cache, k, v, pages, start, count=None, layer: int = 0, stream=None):
         """kvmap_q8_write: rows k, v [layers][B][H][n][d] (or [B][H][n][d] of one layer; device, bf16 or fp32, any
@@ -520,9 +541,9 @@ class Context:
             k, v = k.unsqueeze(0), v.unsqueeze(0)
         if k.dim() != 5:
             raise ValueError("k and v must be [layers][B][H][n][d] or [B][H][n][d]")
-        if k.dtype != v.dtype:
+        if k.dtype is not v.dtype:
             raise TypeError(f"v dtype {v.dtype} differs from k {k.dtype}")
-        self._q8_rows("kvmap_q8_write", cache, k, v, pages, start, k.shape[3], count, layer, _dtype_code(k), stream)
+        self._q8_rows(lib().kvmap_q8_write, cache, k, v, pages, start, k.shape[3], count, layer, _dtype_code(k), stream)
 
     def q8_read(self, cache: Q8Cache, pages, start, n: int, count=None, layer: int = 0, n_layers: int | None = None,
                 dtype=None, out_k=None, out_v=None, stream=None):
@@ -539,7 +560,7 @@ class Context:
             out_v = torch.empty(shape, dtype=dtype, device=cache.k.device)
         if out_k.dtype != dtype or out_v.dtype != dtype:
             raise TypeError("out_k and out_v must be of the dtype asked for")
-        self._q8_rows("kvmap_q8_read", cache, out_k, out_v, pages, start, n, count, layer, _dtype_code(out_k), stream)
+        self._q8_rows(lib().kvmap_q8_read, cache, out_k, out_v, pages, start, n, count, layer, _dtype_code(out_k), stream)
         return out_k, out_v
 
     def q8_dropped(self, stream=None) -> int:
@@ -560,19 +581,24 @@ class Context:
         d^-1/2.  Returns out (allocated if not given), or (out, lse) where lse is a float32 [B][n_q][H_q]
         tensor or True."""
         torch = _torch()
-        if q.dim() != 4 or q.shape[3] != cache.d:
+        shape = q.shape
+        if len(shape) != 4 or shape[3] != cache.d:
             raise ValueError(f"q must be [B][n_q][H_q][{cache.d}]")
-        B, n_q, H_q, d = q.shape
+        B, n_q, H_q, d = shape
         max_pages = pages.shape[-1]
         if out is None:
-            out = torch.empty((B, n_q, H_q, d), dtype=q.dtype, device=q.device)
-        if out.shape != q.shape or out.dtype != q.dtype:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        elif out.shape != shape or out.dtype is not q.dtype:
             raise ValueError("out must match q's shape and dtype")
         if not (q.is_cuda and out.is_cuda):
             raise ValueError("q and out must be device tensors")
-        qs, os_ = q.stride(), out.stride()
-        if qs[3] != 1 or os_[3] != 1:
+        rq, ro = self._rows
+        rq.layer_stride = ro.layer_stride = 0
+        rq.seq_stride, rq.token_stride, rq.head_stride, q_last = q.stride()
+        ro.seq_stride, ro.token_stride, ro.head_stride, out_last = out.stride()
+        if q_last != 1 or out_last != 1:
             raise ValueError("the head dim of q and out must be contiguous")
+        rq.base, ro.base = q.data_ptr(), out.data_ptr()
         lse_ptr = None
         if lse is not None and lse is not False:
             if lse is True:
@@ -580,12 +606,10 @@ class Context:
             elif lse.shape != (B, n_q, H_q) or lse.dtype != torch.float32:
                 raise ValueError("lse must be float32 [B][n_q][H_q]")
             lse_ptr = _dev_ptr(lse, "lse")
-        st = lib().kvmap_q8_attend(self._h, cache.ref, layer, B, n_q, H_q, _dtype_code(q),
-                                   ctypes.byref(Q8RowsC(q.data_ptr(), 0, qs[0], qs[2], qs[1])),
+        st = lib().kvmap_q8_attend(self._h, cache.ref, layer, B, n_q, H_q, _dtype_code(q), self._rows_ref[0],
                                    self._q8_ints(pages, "pages", (B, max_pages)), max_pages,
                                    self._q8_ints(lens, "lens", (B,)), max_len, d ** -0.5 if scale is None else scale,
-                                   ctypes.byref(Q8RowsC(out.data_ptr(), 0, os_[0], os_[2], os_[1])), lse_ptr,
-                                   _stream_handle(stream, q.device))
+                                   self._rows_ref[1], lse_ptr, _stream_of(stream, cache.index))
         if st:
             _check(st, "kvmap_q8_attend")
         return out if lse_ptr is None else (out, lse)
