@@ -21,7 +21,7 @@
 // the score, the value's into the weight.  bf16 calls: bf16 queries; weights in fp16 (11 bits; bf16's 8 would
 // cost the output as much as its own rounding does).  Weights are held as pv = exp2(y2 + log2 v_scale - m) with m
 // the running maximum of that exponent, so pv stays in fp16's range whatever the scales are, and
-// l = sum pv / v_scale.  fp32 calls: queries and weights as three bf16 parts each (24 bits).
+// l = sum pv / v_scale, in 64 bits.  fp32 calls: queries and weights as three bf16 parts each (24 bits).
 
 #include <algorithm>
 
@@ -167,11 +167,12 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
         }
         const int32_t* pages = a.pages + (int64_t)b * a.max_pages;
         f32x4_t o[NT][D / 16];
-        float m[NT], l[NT];
+        float m[NT];
+        double l[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n] = kNone;
-            l[n] = 0.f;
+            l[n] = 0.0;
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) o[n][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
@@ -215,10 +216,8 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
                     for (int n = 0; n < NT; ++n) s[n][mt] = q[n][st].times(k, s[n][mt]);
                 }
             }
-            const int ev = (int)(__float_as_uint(x.vs) >> 23) - 127;
-            const float bias = (float)max(ev, -90);  // (values under 2^-82: l would overflow on their 1 / v_scale)
-            const float small = ev < -90 ? x.vs * 0x1p90f : 1.f;
-            const float back = __uint_as_float((uint32_t)(127 - max(ev, -90)) << 23);  // 1 / v_scale
+            const int ev = scale_exponent(x.vs);
+            const float bias = (float)ev;
             const float cs = x.ks * y2;
             float top[NT];
             bool move = false;
@@ -270,10 +269,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
                     pv[e] = __builtin_amdgcn_exp2f(s[n][e / 4][e % 4] - m[n]);
                     sum += pv[e];
                 }
-                l[n] = fmaf(sum, back, l[n]);
-                if (__any(ev < -90))
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pv[e] *= small;
+                l[n] = fma((double)sum, inverse_scale(ev), l[n]);
                 w[n][0].set(pv);
                 w[n][1].set(pv + 8);
             }
@@ -359,15 +355,21 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
         // join the waves: a fixed order, so the result does not depend on who is first
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float t = l[n];
+            double t = l[n];
             t += __shfl_xor(t, 16);
             t += __shfl_xor(t, 32);
+            float lf;
+            const int down = settle_sum(t, m[n], lf);
             if (g == 0) {
                 s_ml[wave][n * 16 + c][0] = m[n];
-                s_ml[wave][n * 16 + c][1] = t;
+                s_ml[wave][n * 16 + c][1] = lf;
             }
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d) *(f32x4_t*)&s_o[wave][n * 16 + c][16 * d + 4 * g] = o[n][d];
+            for (int d = 0; d < D / 16; ++d) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][d][i] = __builtin_amdgcn_ldexpf(o[n][d][i], down);
+                *(f32x4_t*)&s_o[wave][n * 16 + c][16 * d + 4 * g] = o[n][d];
+            }
         }
         __syncthreads();
         const int rows = min(ROWS, R);

@@ -26,19 +26,19 @@ struct Weights;  // what PV's operands are made of
 // 1 in every byte of w that is a NaN code
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7; }
 
-// 8 codes (two dwords) as a matrix operand, times a power of two
-__device__ __forceinline__ bf16x8_t bf16_codes(uint32_t a, uint32_t b, float by = 1.f) {
-    const bf16x2_t x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, by, false);
-    const bf16x2_t x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, by, true);
-    const bf16x2_t x2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, by, false);
-    const bf16x2_t x3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, by, true);
+// 8 codes (two dwords) as a matrix operand
+__device__ __forceinline__ bf16x8_t bf16_codes(uint32_t a, uint32_t b) {
+    const bf16x2_t x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false);
+    const bf16x2_t x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true);
+    const bf16x2_t x2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false);
+    const bf16x2_t x3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true);
     return bf16x8_t{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
 }
-__device__ __forceinline__ f16x8_t f16_codes(uint32_t a, uint32_t b, float by = 1.f) {
-    const f16x2_t x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, by, false);
-    const f16x2_t x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, by, true);
-    const f16x2_t x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, by, false);
-    const f16x2_t x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, by, true);
+__device__ __forceinline__ f16x8_t f16_codes(uint32_t a, uint32_t b) {
+    const f16x2_t x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, false);
+    const f16x2_t x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, true);
+    const f16x2_t x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, false);
+    const f16x2_t x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, true);
     return f16x8_t{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
 }
 
@@ -74,14 +74,14 @@ struct Weights<true> {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) put(i, x[i], x[i + 1]);
     }
-    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b, float by = 1.f) { return f16_codes(a, b, by); }
+    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b) { return f16_codes(a, b); }
     __device__ __forceinline__ f32x4_t times(Codes v, f32x4_t o) const { return __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p, o, 0, 0, 0); }
     __device__ __forceinline__ f32x16_t times(Codes v, f32x16_t o) const { return __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p, o, 0, 0, 0); }
 };
 template <>
 struct Weights<false> : Parts3 {
     using Codes = bf16x8_t;
-    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b, float by = 1.f) { return bf16_codes(a, b, by); }
+    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b) { return bf16_codes(a, b); }
     __device__ __forceinline__ f32x4_t times(Codes v, f32x4_t o) const {
         o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[2], o, 0, 0, 0);
         o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[1], o, 0, 0, 0);
@@ -175,6 +175,19 @@ __device__ __forceinline__ uint64_t div64(uint64_t a, uint64_t b) {
 
 // A piece's slots: one for an item that it begins (its last), one for an item that began before (its first).
 __host__ __device__ __forceinline__ int64_t q8_slot(int64_t piece, bool begins) { return 2 * piece + begins; }
+
+// A value scale 2^e, and 2^-e.  The sum of a row's weights l = sum exp2(y - m) is held in 64 bits: m follows the largest
+// y + e, and where scales are 2^-110 (a page of zeros) 32 bits would overflow.
+__device__ __forceinline__ int scale_exponent(float s) { return (int)(__float_as_uint(s) >> 23) - 127; }
+__device__ __forceinline__ double inverse_scale(int e) { return __hiloint2double((1023 - e) << 20, 0); }
+
+// A row's sums as they are stored and joined: l in [0.5, 1) with its exponent in m, and the factor 2^-exponent for o.
+__device__ __forceinline__ int settle_sum(double l, float& m, float& lf) {
+    const int e = __builtin_amdgcn_frexp_exp(l);
+    lf = (float)__builtin_amdgcn_frexp_mant(l);
+    m += (float)e;
+    return -e;
+}
 
 // A row's lse; one whose weights sum to 0 saw no token.
 __device__ __forceinline__ float q8_lse(float top, float lsum) { return lsum == 0.f ? -inf32() : (top + __builtin_amdgcn_logf(lsum)) * kLn2; }

@@ -256,8 +256,6 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
         auto store_scale = [&](int tile, float2 sc, int pv) {
             if (tid < 4) s_scale[tile & 3][tid] = pv < 0 || tile * kTile + 16 * tid >= len ? make_float2(nan32(), 1.f) : sc;
         };
-        float vs_next;  // the scale of the values that are stored next
-        auto hold_scale = [&](int tile, float2 sc, int pv) { vs_next = pv < 0 || tile * kTile + 16 * (tid & 3) >= len ? 1.f : sc.y; };
         uint32_t hidden_nan = 0;
         if (tid == 0) s_nan = 0;
         auto clean_v = [&](int tile) {
@@ -280,13 +278,11 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
         };
         auto store_v = [&](int tile) {
             uint8_t* to = s_v + (tile & 1) * (D * VROW);
-            const int ev = (int)(__float_as_uint(vs_next) >> 23) - 127;
-            const float small = ev < -90 ? vs_next * 0x1p90f : 1.f;  // (see bias below)
 #pragma unroll
             for (int j = 0; j < NC; ++j) {
                 auto* w = (typename Weights<BF16>::Codes*)(to + vdim(j) * VROW + 32 * (tid & 3));
-                w[0] = Weights<BF16>::codes(vx[j][0], vx[j][1], small);
-                w[1] = Weights<BF16>::codes(vx[j][2], vx[j][3], small);
+                w[0] = Weights<BF16>::codes(vx[j][0], vx[j][1]);
+                w[1] = Weights<BF16>::codes(vx[j][2], vx[j][3]);
             }
         };
 
@@ -294,21 +290,22 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
         // 16 hi + i in x[n][i].
         f32x16_t even, odd;    // of the halves 2 t and 2 t + 1
         float top;             // the largest of the half that comes next
-        float cs, bias, back;  // its scales, made of
+        float cs, bias;        // its scales, made of
         float2 scl;
+        int ev;                // the value scale's exponent
         int k_at = 0, k_next = KBYTES, k_last = 2 * KBYTES;  // where tiles t, t + 1, t + 2 keep their keys
         auto read_scale = [&](int tile, int mt) { scl = s_scale[tile & 3][2 * mt + hi]; };
         auto use_scale = [&]() {
-            const int ev = (int)(__float_as_uint(scl.y) >> 23) - 127;
+            ev = scale_exponent(scl.y);
             cs = scl.x * y2;
-            bias = (float)max(ev, -90);  // (values under 2^-82: l would overflow on their 1 / v_scale)
-            back = __uint_as_float((uint32_t)(127 - max(ev, -90)) << 23);  // 1 / v_scale
+            bias = (float)ev;
         };
         // Two tiles of keys and one of values into shared memory.  All loads first: they wait for one another only through the
         // page table.
         Query<BF16> q[D / 16];
         f32x16_t o[D / 32];
-        float m = kNone, l = 0.f;
+        float m = kNone;
+        double l = 0.0;
         {
             int pk1[NC];
 #pragma unroll
@@ -336,7 +333,6 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
             }
             store_scale(t0, sc0, pv0);
             store_scale(t0 + 1, sc, pv);
-            hold_scale(t0, sc0, pv0);
             store_k(k_at, k0);
             clean_v(t0);
             store_v(t0);
@@ -414,7 +410,7 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
                     sum[1] = x == 2 ? p[1] : sum[1] + p[1];
                     asm volatile("" : "+v"(sum[0]), "+v"(sum[1]));  // here and not later, with all of p's registers held for it
                     w[(x - 2) / 8].put((x - 2) % 8, p[0], p[1]);
-                    if constexpr (x == E) l = fmaf(sum[0] + sum[1], back, l);
+                    if constexpr (x == E) l = fma((double)(sum[0] + sum[1]), inverse_scale(ev), l);
                 }
                 if constexpr (x < E) p[x & 1] = __builtin_amdgcn_exp2f(fmaf(s[x], cs, shift));
             };
@@ -449,10 +445,7 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
                 // the barrier behind it)
                 if constexpr (mt == 0) {
                     if constexpr (f == NP / 4) load_v(tile + 1);
-                    if constexpr (f == NP / 4 + 1) {
-                        hold_scale(tile + 1, sc, pv);
-                        load_k(tile + 2);
-                    }
+                    if constexpr (f == NP / 4 + 1) load_k(tile + 2);
                     if constexpr (f == NP / 4 + 2) find_pages(tile + 3);
                 } else {
                     if constexpr (f == NP - 4) clean_v(tile + 1);
@@ -487,7 +480,8 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
             const int id = (b * a.c.H + h) * sp.row_blocks + rb;
             sp.cut[sp.few ? id : piece] = make_int2(sp.few ? piece : id, cut.pieces);
         }
-        float sum = l + __shfl_xor(l, 32);
+        float sum;
+        const int down = settle_sum(l + __shfl_xor(l, 32), m, sum);
         if (bad) sum = nan32();
         const int r = rb * BM + wave * 32 + col, i = r / G, hq = h * G + r % G;
         if (r < R && half == 0) {
@@ -509,7 +503,8 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
                     for (int z = 0; z < 4; ++z) {
                         const f32x16_t& x = o[2 * p + d];
                         *(f32x4_t*)(mine + col * LD + 32 * d + 8 * z + 4 * half) =
-                            f32x4_t{x[4 * z] * scale, x[4 * z + 1] * scale, x[4 * z + 2] * scale, x[4 * z + 3] * scale};
+                            f32x4_t{__builtin_amdgcn_ldexpf(x[4 * z], down) * scale, __builtin_amdgcn_ldexpf(x[4 * z + 1], down) * scale,
+                                    __builtin_amdgcn_ldexpf(x[4 * z + 2], down) * scale, __builtin_amdgcn_ldexpf(x[4 * z + 3], down) * scale};
                     }
                 wave_memory();
                 if (whole) {

@@ -557,7 +557,7 @@ class Context:
         if out_k is None:
             out_k = torch.empty(shape, dtype=dtype, device=cache.k.device)
         if out_v is None:
-            out_v = torch.empty(shape, dtype=dtype, device=cache.k.device)
+            out_v = torch.empty_like(out_k, memory_format=torch.contiguous_format)
         if out_k.dtype != dtype or out_v.dtype != dtype:
             raise TypeError("out_k and out_v must be of the dtype asked for")
         self._q8_rows(lib().kvmap_q8_read, cache, out_k, out_v, pages, start, n, count, layer, _dtype_code(out_k), stream)
@@ -602,7 +602,7 @@ class Context:
         lse_ptr = None
         if lse is not None and lse is not False:
             if lse is True:
-                lse = torch.empty((B, n_q, H_q), dtype=torch.float32, device=q.device)
+                lse = q.new_empty((B, n_q, H_q), dtype=torch.float32)
             elif lse.shape != (B, n_q, H_q) or lse.dtype != torch.float32:
                 raise ValueError("lse must be float32 [B][n_q][H_q]")
             lse_ptr = _dev_ptr(lse, "lse")
