@@ -8,7 +8,11 @@
 // Thread layout: d / VEC threads side by side on a token's row (16-byte loads), each holding PASSES
 // consecutive tokens, so that a thread has PASSES tokens of VEC dims in registers: a row's codes
 // leave as they are for keys; for values, whose page is dim-major, a thread's PASSES tokens of one dim
-// are adjacent bytes and the page is turned in LDS.
+// are adjacent bytes and the page is turned in LDS.  A page that a wave can hold so is a wave's, not a
+// workgroup's (bf16 pages of 16 tokens with 64 dims: 1.9 -> 4.0 to 5.2 TB/s written, 2.2 -> 5.2 read).
+//
+// Writing 8,192 mapped tokens of 32 layers takes 590 us, 5.4 TB/s, reading 8 layers of 4 sequences 177 us, 5.7 TB/s;
+// a copy of 4 GiB reaches 4.7 TB/s.  A decode step's write is the launch and one page's way through memory.
 
 #include "common.h"
 #include "internal.h"
@@ -85,7 +89,10 @@ struct Row16 {  // 16 bytes of a row as fp32
     }
 };
 
-// What one workgroup works on.
+// In a scalar register, so that a page's item, its lookups and its addresses stay scalar.
+__device__ __forceinline__ uint32_t wave_of_thread() { return (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / 64)); }
+
+// What one group of threads works on.
 struct Item {
     int j, b, h, layer, kv;
 };
@@ -102,23 +109,65 @@ __device__ __forceinline__ Item item_of(uint32_t i, int n_slots, int B, int H) {
     return t;
 }
 
-template <bool BF16, int D, int P>
+// What a wave's lanes have written, to LDS or the page, is there for the rest of it.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// WAVE: the most 16-byte parts of rows that one wave takes a page of.  512 for writes and 256 for reads, measured on pages of
+// that size: 32 tokens with 128 dims bf16 are written at 5.7 TB/s by waves and 5.2 by workgroups, and read at 5.1 and 5.4.
+template <bool BF16, int D, int P, int WAVE>
 struct Tile {
     static constexpr int ES = BF16 ? 2 : 4;
     static constexpr int VEC = 16 / ES;
-    static constexpr int TPR = D / VEC;                                // threads on a row
-    static constexpr int PASSES = P * TPR > 256 ? P * TPR / 256 : 1;   // consecutive tokens of a thread
-    static constexpr int LDW = P / 4 + 1;                              // LDS dwords of a dim's tokens (odd: spreads the banks)
+    static constexpr int TPR = D / VEC;                          // threads on a row
+    static constexpr int GROUP = P * TPR <= WAVE ? 64 : 256;     // threads on a page
+    static constexpr int PASSES = P * TPR / GROUP;               // consecutive tokens of a thread
+    static constexpr int LDW = P / 4 + 1;                        // LDS dwords of a dim's tokens (odd: spreads the banks)
+    static constexpr int TURN = D * LDW * (256 / GROUP);         // of all groups of a workgroup
+    __device__ static __forceinline__ void sync() {
+        if (GROUP == 256) __syncthreads();
+        else wave_sync();
+    }
 };
 
 template <bool BF16, int D, int P>
-__global__ __launch_bounds__(256) void q8_write_kernel(Q8Pools c, Q8Seqs q, int n_slots, int n, Q8Rows kr, Q8Rows vr,
+using WriteTile = Tile<BF16, D, P, 512>;
+template <bool BF16, int D, int P>
+using ReadTile = Tile<BF16, D, P, 256>;
+
+// The codes of a page's first `lo` tokens rounded to a scale 1 / ratio times as large, by `threads` threads.
+template <int D, int P>
+__device__ __forceinline__ void rescale_page(uint8_t* dst, int kv, int lo, float ratio, int tid, int threads) {
+    if (kv == 0) {
+        for (int i = tid; i < lo * (D / 4); i += threads) {
+            uint32_t* w = (uint32_t*)dst + i;
+            *w = rescale4(*w, ratio);
+        }
+        return;
+    }
+    const int wpd = (lo + 3) / 4;  // dwords of a dim that hold such tokens
+    for (int i = tid; i < D * wpd; i += threads) {
+        const int dim = i / wpd, k = i - dim * wpd;
+        uint32_t* w = (uint32_t*)(dst + dim * P) + k;
+        const uint32_t keep = lo - 4 * k >= 4 ? 0u : 0xFFFFFFFFu << (8 * (lo - 4 * k));
+        *w = (*w & keep) | (rescale4(*w, ratio) & ~keep);
+    }
+}
+
+template <bool BF16, int D, int P>
+__global__ __launch_bounds__(256) void q8_write_kernel(Q8Pools c, Q8Seqs q, int n_slots, uint32_t items, int n, Q8Rows kr, Q8Rows vr,
                                                        unsigned int* __restrict__ dropped) {
-    using T = Tile<BF16, D, P>;
+    using T = WriteTile<BF16, D, P>;
     __shared__ uint32_t s_max[4];
-    __shared__ uint32_t turn[D * T::LDW];
-    const Item it = item_of(blockIdx.x, n_slots, q.B, c.H);
-    const int tid = threadIdx.x;
+    __shared__ uint32_t s_turn[T::TURN];
+    const uint32_t group = T::GROUP == 256 ? 0 : wave_of_thread(), index = blockIdx.x * (256 / T::GROUP) + group;
+    if (index >= items) return;
+    const Item it = item_of(index, n_slots, q.B, c.H);
+    const int tid = threadIdx.x % T::GROUP;
+    uint32_t* turn = s_turn + group * (D * T::LDW);
     const Q8Span sp = q8_span(q.start[it.b], q.count ? q.count[it.b] : n, n, it.j, q.pages + (int64_t)it.b * q.max_pages,
                               q.max_pages, c.n_pages, P);
     if (sp.lo >= sp.live) return;
@@ -149,9 +198,11 @@ __global__ __launch_bounds__(256) void q8_write_kernel(Q8Pools c, Q8Seqs q, int 
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-    if ((tid & 63) == 0) s_max[tid >> 6] = top;
-    __syncthreads();
-    top = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
+    if (T::GROUP == 256) {
+        if ((tid & 63) == 0) s_max[tid >> 6] = top;
+        __syncthreads();
+        top = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
+    }
 
     const int64_t page = it.layer * c.layer_scales + (int64_t)sp.page * c.H + it.h;
     float* scale_at = (it.kv ? c.vs : c.ks) + page;
@@ -162,23 +213,9 @@ __global__ __launch_bounds__(256) void q8_write_kernel(Q8Pools c, Q8Seqs q, int 
         if (before >= scale) {
             scale = before;
         } else {  // the tokens before start are rounded to the new scale
-            const float ratio = before / scale;
-            if (it.kv == 0) {
-                for (int i = tid; i < lo * (D / 4); i += 256) {
-                    uint32_t* w = (uint32_t*)dst + i;
-                    *w = rescale4(*w, ratio);
-                }
-            } else {
-                const int wpd = (lo + 3) / 4;  // dwords of a dim that hold such tokens
-                for (int i = tid; i < D * wpd; i += 256) {
-                    const int dim = i / wpd, k = i - dim * wpd;
-                    uint32_t* w = (uint32_t*)(dst + dim * P) + k;
-                    const uint32_t keep = lo - 4 * k >= 4 ? 0u : 0xFFFFFFFFu << (8 * (lo - 4 * k));
-                    *w = (*w & keep) | (rescale4(*w, ratio) & ~keep);
-                }
-            }
+            rescale_page<D, P>(dst, it.kv, lo, before / scale, tid, T::GROUP);
         }
-        __syncthreads();  // `before` is read, and shared dwords of values are written, before the stores below
+        T::sync();  // `before` is read, and shared dwords of values are written, before the stores below
     }
     if (tid == 0) *scale_at = scale;
     const float inv = 1.f / scale;  // exact: a power of two
@@ -225,8 +262,8 @@ __global__ __launch_bounds__(256) void q8_write_kernel(Q8Pools c, Q8Seqs q, int 
             for (int p = 0; p < T::PASSES; ++p)
                 lds[(col + i) * (T::LDW * 4) + row0 + p] = (uint8_t)(w[p][i / 4] >> (8 * (i & 3)));
     }
-    __syncthreads();
-    for (int i = tid; i < D * (P / 16); i += 256) {
+    T::sync();
+    for (int i = tid; i < D * (P / 16); i += T::GROUP) {
         const int dim = i / (P / 16), k = i % (P / 16);
         const uint32_t* a = turn + dim * T::LDW + 4 * k;
         *(uint4*)(dst + dim * P + 16 * k) = make_uint4(a[0], a[1], a[2], a[3]);
@@ -234,11 +271,14 @@ __global__ __launch_bounds__(256) void q8_write_kernel(Q8Pools c, Q8Seqs q, int 
 }
 
 template <bool BF16, int D, int P>
-__global__ __launch_bounds__(256) void q8_read_kernel(Q8Pools c, Q8Seqs q, int n_slots, int n, Q8Rows kr, Q8Rows vr) {
-    using T = Tile<BF16, D, P>;
-    __shared__ uint32_t turn[D * T::LDW];
-    const Item it = item_of(blockIdx.x, n_slots, q.B, c.H);
-    const int tid = threadIdx.x;
+__global__ __launch_bounds__(256) void q8_read_kernel(Q8Pools c, Q8Seqs q, int n_slots, uint32_t items, int n, Q8Rows kr, Q8Rows vr) {
+    using T = ReadTile<BF16, D, P>;
+    __shared__ uint32_t s_turn[T::TURN];
+    const uint32_t group = T::GROUP == 256 ? 0 : wave_of_thread(), index = blockIdx.x * (256 / T::GROUP) + group;
+    if (index >= items) return;
+    const Item it = item_of(index, n_slots, q.B, c.H);
+    const int tid = threadIdx.x % T::GROUP;
+    uint32_t* turn = s_turn + group * (D * T::LDW);
     const Q8Span sp = q8_span(q.start[it.b], q.count ? q.count[it.b] : n, n, it.j, q.pages + (int64_t)it.b * q.max_pages,
                               q.max_pages, c.n_pages, P);
     if (sp.lo >= sp.hi) return;
@@ -252,7 +292,7 @@ __global__ __launch_bounds__(256) void q8_read_kernel(Q8Pools c, Q8Seqs q, int n
     const float scale = held ? (it.kv ? c.vs : c.ks)[page] : __uint_as_float(0x7FC00000u);
     const int row0 = tid / T::TPR * T::PASSES, col = tid % T::TPR * T::VEC;
     if (it.kv && held && live > lo) {
-        for (int i = tid; i < D * (P / 16); i += 256) {
+        for (int i = tid; i < D * (P / 16); i += T::GROUP) {
             const int dim = i / (P / 16), k = i % (P / 16);
             const uint4 a = *(const uint4*)(src + dim * P + 16 * k);
             uint32_t* w = turn + dim * T::LDW + 4 * k;
@@ -262,7 +302,7 @@ __global__ __launch_bounds__(256) void q8_read_kernel(Q8Pools c, Q8Seqs q, int n
             w[3] = a.w;
         }
     }
-    __syncthreads();
+    T::sync();
     const uint8_t* lds = (const uint8_t*)turn;
 #pragma unroll
     for (int p = 0; p < T::PASSES; ++p) {
@@ -296,38 +336,124 @@ __global__ __launch_bounds__(256) void q8_read_kernel(Q8Pools c, Q8Seqs q, int n
     }
 }
 
+// Writes of at most kFew tokens a sequence: a wave takes a page, its lanes D / 64 dims of every row that enters, so that a
+// page's other rows cost nothing.  A token of 16 sequences in 40 layers: 13 us in bf16 pages of 64 and in fp32 ones of 128,
+// 33 and 49 in the kernel above.  Eight tokens of 4 sequences in 8 layers take 7.6 us here and 8.1 there; the lanes' loads
+// are 4 bytes, not 16, and eight rows fill their registers.
+constexpr int kFew = 8;
+template <bool BF16, int D, int P>
+__global__ __launch_bounds__(256) void q8_write_few_kernel(Q8Pools c, Q8Seqs q, int n_slots, uint32_t items, int n, Q8Rows kr, Q8Rows vr,
+                                                           unsigned int* __restrict__ dropped) {
+    constexpr int V = D / 64, ES = BF16 ? 2 : 4;
+    const uint32_t index = blockIdx.x * 4 + wave_of_thread();
+    if (index >= items) return;
+    const Item it = item_of(index, n_slots, q.B, c.H);
+    const int lane = threadIdx.x & 63;
+    const Q8Span sp = q8_span(q.start[it.b], q.count ? q.count[it.b] : n, n, it.j, q.pages + (int64_t)it.b * q.max_pages,
+                              q.max_pages, c.n_pages, P);
+    if (sp.lo >= sp.live) return;
+    if (sp.page < 0) {
+        if (lane == 0 && (!sp.bad_seq || it.j == 0)) atomicAdd(dropped, 1u);
+        return;
+    }
+    const int lo = sp.lo, rows = sp.live - lo;
+    const int64_t page = it.layer * c.layer_scales + (int64_t)sp.page * c.H + it.h;
+    float* scale_at = (it.kv ? c.vs : c.ks) + page;
+    uint8_t* dst = (it.kv ? c.v : c.k) + page * (P * D);
+    const float before = lo ? *scale_at : 0.f;
+    const Q8Rows& r = it.kv ? vr : kr;
+    const char* src = (const char*)r.base +
+                      (it.layer * r.layer + it.b * r.seq + it.h * r.head + (sp.p0 + lo) * r.token + lane * V) * ES;
+    float x[kFew][V];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) {
+        if (i >= rows) break;
+        const char* at = src + i * r.token * ES;
+        if (BF16 && V == 2) {
+            const uint32_t w = *(const uint32_t*)at;
+            x[i][0] = bf16lo(w);
+            x[i][V - 1] = bf16hi(w);
+        } else if (BF16) {
+            x[i][0] = __uint_as_float((uint32_t)*(const uint16_t*)at << 16);
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) x[i][k] = ((const float*)at)[k];
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const uint32_t u = __float_as_uint(x[i][k]) & 0x7FFFFFFFu;
+            top = max(top, u < 0x7F800000u ? u : 0u);
+        }
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    float scale = scale_for(__uint_as_float(top));
+    if (lo) {
+        if (before >= scale) scale = before;
+        else rescale_page<D, P>(dst, it.kv, lo, before / scale, lane, 64);
+        wave_sync();  // dwords of values that also hold new tokens are written before the bytes below
+    }
+    if (lane == 0) *scale_at = scale;
+    const float inv = 1.f / scale;  // exact: a power of two
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) {
+        if (i >= rows) break;
+        float y[4] = {x[i][0], x[i][V - 1], 0.f, 0.f};
+        const uint32_t w = codes4(y, inv);
+        if (it.kv) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) dst[(lane * V + k) * P + lo + i] = (uint8_t)(w >> (8 * k));
+        } else if (V == 2) {
+            *(uint16_t*)(dst + (lo + i) * D + 2 * lane) = (uint16_t)w;
+        } else {
+            dst[(lo + i) * D + lane] = (uint8_t)w;
+        }
+    }
+}
+
 // A row range of n tokens touches at most this many pages.
 int slots(int n, int page) { return (int)(((int64_t)n + 2 * page - 2) / page); }
 
 }  // namespace
 
-#define KVMAP_Q8_PAGES(KERNEL, ...)                                                                         \
-    do {                                                                                                    \
-        const int ns = slots(n, c.page);                                                                    \
-        const dim3 grid((unsigned)((int64_t)ns * q.B * c.H * n_layers * 2));                                \
-        if (e == Elem::BF16) {                                                                              \
-            if (c.d == 128) KVMAP_Q8_P(KERNEL, true, 128, __VA_ARGS__); else KVMAP_Q8_P(KERNEL, true, 64, __VA_ARGS__); \
-        } else {                                                                                            \
-            if (c.d == 128) KVMAP_Q8_P(KERNEL, false, 128, __VA_ARGS__); else KVMAP_Q8_P(KERNEL, false, 64, __VA_ARGS__); \
-        }                                                                                                   \
-    } while (0)
-#define KVMAP_Q8_P(KERNEL, B, D, ...)                                                                           \
+// KERNEL<bf16, d, page> over the items of a call, GROUP threads on each.
+#define KVMAP_Q8_PAGES(KERNEL, GROUP, ...)                                                                      \
     do {                                                                                                        \
-        if (c.page == 16) hipLaunchKernelGGL((KERNEL<B, D, 16>), grid, dim3(256), 0, s, c, q, ns, n, __VA_ARGS__);       \
-        else if (c.page == 32) hipLaunchKernelGGL((KERNEL<B, D, 32>), grid, dim3(256), 0, s, c, q, ns, n, __VA_ARGS__);  \
-        else if (c.page == 64) hipLaunchKernelGGL((KERNEL<B, D, 64>), grid, dim3(256), 0, s, c, q, ns, n, __VA_ARGS__);  \
-        else hipLaunchKernelGGL((KERNEL<B, D, 128>), grid, dim3(256), 0, s, c, q, ns, n, __VA_ARGS__);                   \
+        const int ns = slots(n, c.page);                                                                        \
+        const uint32_t items = (uint32_t)((int64_t)ns * q.B * c.H * n_layers * 2);                              \
+        if (e == Elem::BF16) {                                                                                  \
+            if (c.d == 128) KVMAP_Q8_P(KERNEL, GROUP, true, 128, __VA_ARGS__);                                  \
+            else KVMAP_Q8_P(KERNEL, GROUP, true, 64, __VA_ARGS__);                                              \
+        } else {                                                                                                \
+            if (c.d == 128) KVMAP_Q8_P(KERNEL, GROUP, false, 128, __VA_ARGS__);                                 \
+            else KVMAP_Q8_P(KERNEL, GROUP, false, 64, __VA_ARGS__);                                             \
+        }                                                                                                       \
     } while (0)
+#define KVMAP_Q8_P(KERNEL, GROUP, B, D, ...)                                                                    \
+    do {                                                                                                        \
+        if (c.page == 16) KVMAP_Q8_L(KERNEL, GROUP, B, D, 16, __VA_ARGS__);                                     \
+        else if (c.page == 32) KVMAP_Q8_L(KERNEL, GROUP, B, D, 32, __VA_ARGS__);                                \
+        else if (c.page == 64) KVMAP_Q8_L(KERNEL, GROUP, B, D, 64, __VA_ARGS__);                                \
+        else KVMAP_Q8_L(KERNEL, GROUP, B, D, 128, __VA_ARGS__);                                                 \
+    } while (0)
+#define KVMAP_Q8_L(KERNEL, GROUP, B, D, P, ...)                                                                 \
+    hipLaunchKernelGGL((KERNEL<B, D, P>), dim3((items + 256 / GROUP(B, D, P) - 1) / (256 / GROUP(B, D, P))), dim3(256), 0, s, c, q, ns, \
+                       items, n, __VA_ARGS__)
+#define KVMAP_Q8_WRITE_GROUP(B, D, P) (WriteTile<B, D, P>::GROUP)
+#define KVMAP_Q8_READ_GROUP(B, D, P) (ReadTile<B, D, P>::GROUP)
+#define KVMAP_Q8_WAVE(B, D, P) 64
 
 hipError_t launch_q8_write(Elem e, const Q8Pools& c, const Q8Seqs& q, int n_layers, int n, const Q8Rows& k,
                            const Q8Rows& v, unsigned int* dropped, hipStream_t s) {
-    KVMAP_Q8_PAGES(q8_write_kernel, k, v, dropped);
+    if (n <= kFew) KVMAP_Q8_PAGES(q8_write_few_kernel, KVMAP_Q8_WAVE, k, v, dropped);
+    else KVMAP_Q8_PAGES(q8_write_kernel, KVMAP_Q8_WRITE_GROUP, k, v, dropped);
     return hipGetLastError();
 }
 
 hipError_t launch_q8_read(Elem e, const Q8Pools& c, const Q8Seqs& q, int n_layers, int n, const Q8Rows& k,
                           const Q8Rows& v, hipStream_t s) {
-    KVMAP_Q8_PAGES(q8_read_kernel, k, v);
+    KVMAP_Q8_PAGES(q8_read_kernel, KVMAP_Q8_READ_GROUP, k, v);
     return hipGetLastError();
 }
 
