@@ -9,7 +9,7 @@
 // consecutive tokens, so that a thread has PASSES tokens of VEC dims in registers: a row's codes
 // leave as they are for keys; for values, whose page is dim-major, a thread's PASSES tokens of one dim
 // are adjacent bytes and the page is turned in LDS.  A page that a wave can hold so is a wave's, not a
-// workgroup's (bf16 pages of 16 tokens with 64 dims: 1.9 -> 4.0 to 5.2 TB/s written, 2.2 -> 5.2 read).
+// workgroup's (bf16 pages of 16 tokens with 64 dims: 1.9 -> 4.0 to 5.2 TB/s written, 2.2 -> 5.3 read).
 //
 // Writing 8,192 mapped tokens of 32 layers takes 590 us, 5.4 TB/s, reading 8 layers of 4 sequences 177 us, 5.7 TB/s;
 // a copy of 4 GiB reaches 4.7 TB/s.  A decode step's write is the launch and one page's way through memory.
@@ -116,8 +116,9 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// WAVE: the most 16-byte parts of rows that one wave takes a page of.  512 for writes and 256 for reads, measured on pages of
-// that size: 32 tokens with 128 dims bf16 are written at 5.7 TB/s by waves and 5.2 by workgroups, and read at 5.1 and 5.4.
+// WAVE: the most 16-byte parts of rows that one wave takes a page of.  Measured on pages of 512 parts, by waves and by
+// workgroups: writes 5.7 and 5.2 TB/s (bf16, 32 tokens of 128 dims), fp32 reads 5.5 and 4.8 (32 tokens of 64), bf16 reads 5.2
+// and 5.6.
 template <bool BF16, int D, int P, int WAVE>
 struct Tile {
     static constexpr int ES = BF16 ? 2 : 4;
@@ -136,7 +137,7 @@ struct Tile {
 template <bool BF16, int D, int P>
 using WriteTile = Tile<BF16, D, P, 512>;
 template <bool BF16, int D, int P>
-using ReadTile = Tile<BF16, D, P, 256>;
+using ReadTile = Tile<BF16, D, P, BF16 ? 256 : 512>;
 
 // The codes of a page's first `lo` tokens rounded to a scale 1 / ratio times as large, by `threads` threads.
 template <int D, int P>
@@ -255,13 +256,11 @@ __global__ __launch_bounds__(256) void q8_write_kernel(Q8Pools c, Q8Seqs q, int 
         return;
     }
     uint8_t* lds = (uint8_t*)turn;
-    if (row0 < P) {
 #pragma unroll
-        for (int i = 0; i < T::VEC; ++i)
+    for (int i = 0; i < T::VEC; ++i)
 #pragma unroll
-            for (int p = 0; p < T::PASSES; ++p)
-                lds[(col + i) * (T::LDW * 4) + row0 + p] = (uint8_t)(w[p][i / 4] >> (8 * (i & 3)));
-    }
+        for (int p = 0; p < T::PASSES; ++p)
+            lds[(col + i) * (T::LDW * 4) + row0 + p] = (uint8_t)(w[p][i / 4] >> (8 * (i & 3)));
     T::sync();
     for (int i = tid; i < D * (P / 16); i += T::GROUP) {
         const int dim = i / (P / 16), k = i % (P / 16);
@@ -291,6 +290,13 @@ __global__ __launch_bounds__(256) void q8_read_kernel(Q8Pools c, Q8Seqs q, int n
     const uint8_t* src = (it.kv ? c.v : c.k) + page * (P * D);
     const float scale = held ? (it.kv ? c.vs : c.ks)[page] : __uint_as_float(0x7FC00000u);
     const int row0 = tid / T::TPR * T::PASSES, col = tid % T::TPR * T::VEC;
+    uint32_t w[T::PASSES][T::VEC / 4];  // keys: all of a thread's loads before its first store
+    if (it.kv == 0 && held && live > lo) {
+#pragma unroll
+        for (int p = 0; p < T::PASSES; ++p)
+#pragma unroll
+            for (int g = 0; g < T::VEC / 4; ++g) w[p][g] = *(const uint32_t*)(src + (row0 + p) * D + col + 4 * g);
+    }
     if (it.kv && held && live > lo) {
         for (int i = tid; i < D * (P / 16); i += T::GROUP) {
             const int dim = i / (P / 16), k = i % (P / 16);
@@ -318,14 +324,11 @@ __global__ __launch_bounds__(256) void q8_read_kernel(Q8Pools c, Q8Seqs q, int n
         } else {
 #pragma unroll
             for (int g = 0; g < T::VEC / 4; ++g) {
-                uint32_t w;
-                if (it.kv == 0) {
-                    w = *(const uint32_t*)(src + row * D + col + 4 * g);
-                } else {
+                if (it.kv) {
                     const uint8_t* a = lds + (col + 4 * g) * (T::LDW * 4) + row;
-                    w = a[0] | (uint32_t)a[T::LDW * 4] << 8 | (uint32_t)a[2 * T::LDW * 4] << 16 | (uint32_t)a[3 * T::LDW * 4] << 24;
+                    w[p][g] = a[0] | (uint32_t)a[T::LDW * 4] << 8 | (uint32_t)a[2 * T::LDW * 4] << 16 | (uint32_t)a[3 * T::LDW * 4] << 24;
                 }
-                values4(w, f + 4 * g);
+                values4(w[p][g], f + 4 * g);
             }
 #pragma unroll
             for (int i = 0; i < T::VEC; ++i) f[i] *= scale;
