@@ -196,6 +196,7 @@ struct Q8Attend {
     float scale;
     Q8Rows q, out;
     float* lse;
+    int inv_g;  // 65536 / G + 1, G = Hq / c.H: r / G is r * inv_g >> 16 for r < 65536 / G
 };
 // The launch of one attention call: fixed by the host's sizes alone.
 struct Q8Plan {

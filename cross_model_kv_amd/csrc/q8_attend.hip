@@ -97,6 +97,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
     __shared__ float s_ml[kWaves][ROWS][2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.Hq / a.c.H, R = a.n_q * G;
+    const int inv_g = a.inv_g;  // r / G = r * inv_g >> 16 for the rows here
     const int P = a.c.page, logP = 31 - __clz(P);
     const int items = a.c.H;  // of one sequence
     const float y2 = a.scale * kLog2e;
@@ -147,6 +148,16 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
         const int c = x0 & 15, g = (x0 & 63) >> 4;
         const int t_begin = s_begin * kWaves, t_end = min(tiles, s_end * kWaves);
 
+        const int32_t* pages = a.pages + (int64_t)b * a.max_pages;
+        // the pages of the 16 tokens that this lane's key rows and its values come from
+        auto pages_of = [&](int tile, int& pk, int& pv) {
+            pk = q8_page_at(pages, (tile * kTile + 16 * (c >> 2)) >> logP, a.max_pages, a.c.n_pages);
+            pv = q8_page_at(pages, (tile * kTile + 16 * g) >> logP, a.max_pages, a.c.n_pages);
+        };
+        int tile = t_begin + wave, pk = -1, pv = -1;
+        if (tile < t_end) pages_of(tile, pk, pv);  // (on their way while the queries are found)
+        __builtin_amdgcn_sched_barrier(0);
+
         // this lane's rows: their queries, and the tokens that they see
         Query<BF16> q[NT][D / 32];
         int end[NT];
@@ -154,7 +165,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = n * 16 + c;
-            const int i = r / G, hq = h * G + r % G;
+            const int i = r * inv_g >> 16, hq = h * G + r - i * G;
             end[n] = len - a.n_q + i + 1;
 #pragma unroll
             for (int s = 0; s < D / 32; ++s) {
@@ -165,7 +176,6 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
                     q[n][s].zero();
             }
         }
-        const int32_t* pages = a.pages + (int64_t)b * a.max_pages;
         f32x4_t o[NT][D / 16];
         float m[NT];
         double l[NT];
@@ -177,11 +187,6 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
             for (int t = 0; t < D / 16; ++t) o[n][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
 
-        // the pages of the 16 tokens that this lane's key rows and its values come from
-        auto pages_of = [&](int tile, int& pk, int& pv) {
-            pk = q8_page_at(pages, (tile * kTile + 16 * (c >> 2)) >> logP, a.max_pages, a.c.n_pages);
-            pv = q8_page_at(pages, (tile * kTile + 16 * g) >> logP, a.max_pages, a.c.n_pages);
-        };
         auto load = [&](int tile, int pk, int pv, TileData<D>& x) {
             const int tk = tile * kTile + 16 * (c >> 2) + (c & 3), tv = tile * kTile + 16 * g;
             const int64_t pgk = (int64_t)max(pk, 0) * a.c.H + h, pgv = (int64_t)max(pv, 0) * a.c.H + h;
@@ -306,16 +311,11 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
             }
         };
 
-        int tile = t_begin + wave;
-        if (tile < t_end) {
-            int pk, pv;
-            pages_of(tile, pk, pv);
-            for (; tile < t_end; tile += kWaves) {
-                TileData<D> x;
-                load(tile, pk, pv, x);
-                pages_of(tile + kWaves, pk, pv);
-                step(tile, x);
-            }
+        for (; tile < t_end; tile += kWaves) {
+            TileData<D> x;
+            load(tile, pk, pv, x);
+            pages_of(tile + kWaves, pk, pv);
+            step(tile, x);
         }
 
         // Rows that see a NaN value taken out above: which dims of which rows is the product of where the NaNs are
@@ -371,13 +371,13 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
                 *(f32x4_t*)&s_o[wave][n * 16 + c][16 * d + 4 * g] = o[n][d];
             }
         }
-        __syncthreads();
-        const int rows = min(ROWS, R);
         asm volatile("" : "+v"(x0));  // (nor across the loop above)
-        if (x0 == 0 && sp.cut && s_begin == 0) {  // (of several items that begin here only the last may be cut)
+        if (x0 == 255 && sp.cut && s_begin == 0) {  // (of several items that begin here only the last may be cut)
             const int pieces = (int)div64(item_at + steps - 1, share) - (int)blockIdx.x + 1, id = b * items + h;
             sp.cut[sp.few ? id : (int)blockIdx.x] = make_int2(sp.few ? (int)blockIdx.x : id, pieces);
         }
+        __syncthreads();
+        const int rows = min(ROWS, R);
         if (s_begin > 0 || s_end < steps) {
             const int64_t slot = q8_slot(blockIdx.x, s_begin == 0) * ROWS;
             for (int x = x0; x < rows * (D / 4); x += 256) {
@@ -395,7 +395,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
                 f32x4_t sum;
                 join_waves<ROWS, LDO>(s_o, s_ml, row, d4, top, lsum, sum);
                 if (bad) lsum = nan32();
-                q8_store_row<BF16>(a, b, row / G, h * G + row % G, d4, top, lsum, sum);
+                q8_store_row<BF16>(a, b, row * inv_g >> 16, h * G + row - (row * inv_g >> 16) * G, d4, top, lsum, sum);
             }
         }
         at = item_at + s_end;
