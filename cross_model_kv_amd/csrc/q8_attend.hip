@@ -22,6 +22,12 @@
 // cost the output as much as its own rounding does).  Weights are held as pv = exp2(y2 + log2 v_scale - m) with m
 // the running maximum of that exponent, so pv stays in fp16's range whatever the scales are, and
 // l = sum pv / v_scale, in 64 bits.  fp32 calls: queries and weights as three bf16 parts each (24 bits).
+//
+// What bounds it: bytes, where there are enough of them.  64 sequences of up to 16,384 tokens, 64 query and 8 KV heads: 1.08 GB
+// in 205 us, 5.2 TB/s (a copy of 4 GiB reaches 4.75); 32,768 tokens of one: 67 MB in 17.7 us and 4 to join.  Below some
+// thousand tokens a sequence it is the way through one step: 3,000 cycles until a workgroup knows its piece, 2,000 for
+// its item and queries, 5,000 to 8,000 a tile (900 instructions at 4.5 cycles, and the CU's 64 bytes a cycle), 3,000 to join the
+// waves and store: 7.2 us for 130 tokens.
 
 #include <algorithm>
 
@@ -50,6 +56,11 @@ struct TileData {
 // stops at two row tiles and a test reads every instance's scratch size.
 template <bool BF16, int D, int NT>
 constexpr int kOccupancy = BF16 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 2 : 1);
+
+// Workgroups that a CU holds at once, as the registers (kOccupancy) and the shared memory allow.
+__host__ __device__ constexpr int per_cu(bool bf16, int nt) { return bf16 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 2 : 1); }
+template <bool BF16, int NT>
+constexpr bool kThird = per_cu(BF16, NT) == 3;
 
 // Sums of the lanes up to and including one's own.
 __device__ __forceinline__ uint32_t wave_scan(uint32_t x, int lane) {
@@ -107,7 +118,17 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
     uint64_t total = __builtin_amdgcn_readlane(upto, 63);
     for (int b0 = 64; b0 < a.B; b0 += 64) total += __shfl(steps_upto(a, b0, a.B, lane), 63);
     total *= items;
-    const uint64_t share = div64(total + gridDim.x - 1, gridDim.x);
+    uint64_t share = 1;
+    if (total > gridDim.x) {
+        share = div64(total + gridDim.x - 1, gridDim.x);
+        if (kThird<BF16, NT>) {
+            // Of three workgroups a CU the third may go at once: two move 4 % more bytes a second (64 sequences of up to 16,384
+            // tokens 201 us, by three 209), and the pieces' whole steps may fit better (64 of 1,000: 34 and 40 us; 48 of
+            // 1,000: 32 and 29).
+            const uint64_t two = gridDim.x - gridDim.x / 3, share2 = div64(total + two - 1, two);
+            if (2 * share2 < 3 * share + share / 8) share = share2;
+        }
+    }
     uint64_t at = share * blockIdx.x;
     const uint64_t stop = at + share < total ? at + share : total;
     if (tid == 0 && sp.cut && !sp.few) sp.cut[blockIdx.x] = make_int2(0, 1);
@@ -402,9 +423,6 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
         __syncthreads();  // the next item's sums come into the same memory
     }
 }
-
-// Workgroups that a CU holds at once, as the registers (kOccupancy) and the shared memory allow.
-constexpr int per_cu(bool bf16, int nt) { return bf16 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 2 : 1); }
 
 }  // namespace
 

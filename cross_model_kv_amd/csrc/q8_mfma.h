@@ -97,8 +97,8 @@ struct Weights<false> : Parts3 {
 // s (+)= k q with s in vector registers and q in accumulation registers.  Where a kernel may use accumulation registers the
 // compiler puts every product's result there, and moves what vector instructions need of it, one register an instruction:
 // a quarter of the vector work of a tile.  Written out, the compiler does not know that it is a matrix product, whose result
-// may not be read by a vector instruction within 11 instructions (8 passes): the caller keeps them apart, and
-// tests/test_q8_boundary.py reads the listing for it.
+// may not be touched by a vector instruction close behind it (8 passes): the caller keeps them apart, and
+// tests/test_q8_listing.py reads the listing for 13 instructions between them.
 template <bool FIRST>
 __device__ __forceinline__ void mfma_to_vector(bf16x8_t k, bf16x8_t q, f32x16_t& s) {
     if (FIRST) asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(s) : "v"(k), "a"(q));

@@ -563,9 +563,10 @@ int kvmap_q8_dropped(kvmap_ctx* ctx, uint32_t* n, void* stream);
  * A sequence whose len is out of range (negative, above max_len or max_pages * page) gives NaN, and so does a
  * row that sees a token of a page outside 0 .. n_pages - 1.
  * bf16: products with bf16 queries and fp16 softmax weights on the matrix cores (11 bits, so that the output's
- * own rounding is what counts), sums and statistics in fp32.  fp32: queries and weights as three bf16 parts each,
- * so that products keep 24 bits.
- * Repeated calls give identical outputs.  Asynchronous on `stream`.  Long caches are split over workgroups
+ * own rounding is what counts), products' sums and statistics in fp32, the sum of a row's weights in fp64 (it spans the
+ * values' scales).  fp32: queries and weights as three bf16 parts each, so that products keep 24 bits.
+ * Repeated calls give identical outputs.  (Where a long cache is cut follows the lengths of all sequences, so a sequence's
+ * rounding may differ between calls with different company.)  Asynchronous on `stream`.  Long caches are split over workgroups
  * whose results are joined through a scratch buffer that the context owns: of one size for all calls, allocated
  * by kvmap_q8_reserve or by the first call that needs it, and kept until kvmap_destroy.  A call that would have to
  * allocate it while `stream` is being captured is refused (INVALID_ARGUMENT).  Errors as kvmap_q8_write. */
