@@ -131,7 +131,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
     }
     uint64_t at = share * blockIdx.x;
     const uint64_t stop = at + share < total ? at + share : total;
-    if (tid == 0 && sp.cut && !sp.few) sp.cut[blockIdx.x] = make_int2(0, 1);
+    if (tid == 255 && sp.cut && !sp.few) sp.cut[blockIdx.x] = make_int2(0, 1);  // (by the thread that may write it again)
     if (at >= stop) return;
     int b = 0;
     uint64_t base = 0;  // the sequence's first step

@@ -500,8 +500,8 @@ typedef struct {
 } kvmap_q8_cache;
 
 /* The sequences of a call.  Token t of sequence b lives in page pages[b * max_pages + t / page], row
- * t % page.  Entries past a sequence's last token are not read.  No page may belong to two sequences
- * of one write. */
+ * t % page.  What entries past a sequence's last token hold does not matter.  No page may belong to two
+ * sequences of one write. */
 typedef struct {
     int32_t B, max_pages;
     const int32_t* pages; /* device [B][max_pages]                                       */
