@@ -196,7 +196,8 @@ struct Q8Attend {
     float scale;
     Q8Rows q, out;
     float* lse;
-    int inv_g;  // 65536 / G + 1, G = Hq / c.H: r / G is r * inv_g >> 16 for r < 65536 / G
+    int g_shift;      // rows' division by G = Hq / c.H: r / G = r * g_mul >> g_shift for r < 2^28 (q8_divisor, q8_query)
+    uint32_t g_mul;
 };
 // The launch of one attention call: fixed by the host's sizes alone.
 struct Q8Plan {

@@ -8,6 +8,7 @@
 #include <utility>
 
 #include "internal.h"
+#include "q8_span.h"
 
 using namespace kvmap;
 
@@ -325,8 +326,8 @@ extern "C" int kvmap_q8_attend(kvmap_ctx* ctx, const kvmap_q8_cache* c, int32_t 
     Q8State* s = q8_state(ctx);
     OnDevice on(s->device);
     if (!on.okay) return report(KVMAP_ERR_DEVICE, "kvmap_q8_attend: hipSetDevice(%d) failed", s->device);
-    Q8Attend a{pools(c, layer), pages, len, B, n_q, H_q, max_pages, max_len, (float)scale, rows(q), rows(out), lse,
-               65536 / (H_q / c->H_kv) + 1};
+    Q8Attend a{pools(c, layer), pages, len, B, n_q, H_q, max_pages, max_len, (float)scale, rows(q), rows(out), lse, 0, 0};
+    q8_divisor((uint32_t)(H_q / c->H_kv), a.g_mul, a.g_shift);
     const Q8Plan plan = q8_attend_plan(dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32, B, n_q, H_q, c->H_kv, c->head_dim, max_len, s->cus);
     if (plan.splits) {
         const int r = ensure_scratch(s, (hipStream_t)stream, true);

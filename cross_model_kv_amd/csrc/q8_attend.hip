@@ -108,7 +108,6 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
     __shared__ float s_ml[kWaves][ROWS][2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.Hq / a.c.H, R = a.n_q * G;
-    const int inv_g = a.inv_g;  // r / G = r * inv_g >> 16 for the rows here
     const int P = a.c.page, logP = 31 - __clz(P);
     const int items = a.c.H;  // of one sequence
     const float y2 = a.scale * kLog2e;
@@ -186,7 +185,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = n * 16 + c;
-            const int i = r * inv_g >> 16, hq = h * G + r - i * G;
+            const int i = q8_query(a, r), hq = h * G + r - i * G;
             end[n] = len - a.n_q + i + 1;
 #pragma unroll
             for (int s = 0; s < D / 32; ++s) {
@@ -416,7 +415,8 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
                 f32x4_t sum;
                 join_waves<ROWS, LDO>(s_o, s_ml, row, d4, top, lsum, sum);
                 if (bad) lsum = nan32();
-                q8_store_row<BF16>(a, b, row * inv_g >> 16, h * G + row - (row * inv_g >> 16) * G, d4, top, lsum, sum);
+                const int i = q8_query(a, row);
+                q8_store_row<BF16>(a, b, i, h * G + row - i * G, d4, top, lsum, sum);
             }
         }
         at = item_at + s_end;

@@ -76,7 +76,8 @@ __global__ __launch_bounds__(256) void q8_join_kernel(Q8Attend a, Q8Pieces sp) {
             sum += f * s_o[k][threadIdx.x];
         }
     }
-    q8_store_row<BF16>(a, b, r / G, h * G + r % G, d4, top, lsum, sum);
+    const int i = q8_query(a, r);
+    q8_store_row<BF16>(a, b, i, h * G + r - i * G, d4, top, lsum, sum);
 }
 
 }  // namespace

@@ -4,6 +4,7 @@
 
 #include "common.h"
 #include "internal.h"
+#include "q8_span.h"
 
 namespace kvmap {
 namespace {
@@ -188,6 +189,9 @@ __device__ __forceinline__ int settle_sum(double l, float& m, float& lf) {
     m += (float)e;
     return -e;
 }
+
+// The query of a row.
+__device__ __forceinline__ int q8_query(const Q8Attend& a, int r) { return q8_divide(r, a.g_mul, a.g_shift); }
 
 // A row's lse; one whose weights sum to 0 saw no token.
 __device__ __forceinline__ float q8_lse(float top, float lsum) { return lsum == 0.f ? -inf32() : (top + __builtin_amdgcn_logf(lsum)) * kLn2; }

@@ -43,7 +43,7 @@ constexpr int kTile = 64;
 // Tokens that the last row of a row block sees, and its tiles: one at least, so that its rows are answered.
 __device__ __forceinline__ int block_end(const Q8Attend& a, int G, int len, int rb, int bm) {
     const int last = min((rb + 1) * bm, a.n_q * G) - 1;
-    return len - a.n_q + last / G + 1;
+    return len - a.n_q + q8_query(a, last) + 1;
 }
 __device__ __forceinline__ int block_tiles(const Q8Attend& a, int G, int len, int rb, int bm) {
     if (len < 1 || len > a.max_len) return 1;
@@ -196,13 +196,14 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
         if (again) __syncthreads();  // this item's tiles come into the memory of the one before
         again = true;
         const bool bad = len < 0 || len > a.max_len;
-        const int first_end = bad ? 0 : len - a.n_q + rb * BM / G + 1;               // the fewest tokens that a row sees
-        const int wave_end = bad ? 0 : len - a.n_q + (rb * BM + wave * 32) / G + 1;  // the same of the wave's rows
+        const int first_end = bad ? 0 : len - a.n_q + q8_query(a, rb * BM) + 1;               // the fewest tokens that a row sees
+        const int wave_end = bad ? 0 : len - a.n_q + q8_query(a, rb * BM + wave * 32) + 1;  // the same of the wave's rows
         const int32_t* pages = a.pages + (int64_t)b * a.max_pages;
 
         const int tid = 64 * wave + fresh_lane(), c = tid & 31, hi = tid >> 5 & 1;
         const int row = rb * BM + wave * 32 + c;  // of the sequence and head
-        const int end = bad ? 0 : min(len - a.n_q + row / G + 1, len);
+        const int query = q8_query(a, row);  // (rows past the last are fewer than 2^28 too)
+        const int end = bad ? 0 : min(len - a.n_q + query + 1, len);
 
         // A thread's part of a tile: keys as 16 dims of the tokens ktok(j), values as 16 tokens (group tid & 3) of the dims
         // vdim(j), and the group's scales.
@@ -325,7 +326,7 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
             pg = pg1;
             load_k(t0 + 1);
             find_pages(t0 + 2);
-            const int64_t q_at = (int64_t)b * a.q.seq + (int64_t)(h * G + row % G) * a.q.head + (int64_t)(row / G) * a.q.token + 8 * hi;
+            const int64_t q_at = (int64_t)b * a.q.seq + (int64_t)(h * G + row - query * G) * a.q.head + (int64_t)query * a.q.token + 8 * hi;
 #pragma unroll
             for (int st = 0; st < D / 16; ++st) {
                 if (row < R) q[st].load(a.q.base, q_at + 16 * st);
@@ -483,7 +484,7 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
         float sum;
         const int down = settle_sum(l + __shfl_xor(l, 32), m, sum);
         if (bad) sum = nan32();
-        const int r = rb * BM + wave * 32 + col, i = r / G, hq = h * G + r % G;
+        const int r = rb * BM + wave * 32 + col, i = q8_query(a, r), hq = h * G + r - i * G;
         if (r < R && half == 0) {
             if (!whole) *(float2*)(sp.part_ml + slot * 2) = make_float2(m, sum);
             else if (a.lse) a.lse[((int64_t)b * a.n_q + i) * a.Hq + hq] = q8_lse(m, sum);
@@ -512,7 +513,8 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
                     for (int k = 0; k < 32 * 64 / (64 * DIMS); ++k) {
                         const int y = (k * 64 + own) / (64 / DIMS), at = own % (64 / DIMS) * DIMS, ry = rb * BM + wave * 32 + y;
                         if (ry >= R) continue;
-                        const int64_t to = (int64_t)b * a.out.seq + (int64_t)(h * G + ry % G) * a.out.head + (int64_t)(ry / G) * a.out.token + 64 * p + at;
+                        const int iy = q8_query(a, ry);
+                        const int64_t to = (int64_t)b * a.out.seq + (int64_t)(h * G + ry - iy * G) * a.out.head + (int64_t)iy * a.out.token + 64 * p + at;
                         const f32x4_t x0 = *(const f32x4_t*)(mine + y * LD + at);
                         if (BF16) {
                             const f32x4_t x1 = *(const f32x4_t*)(mine + y * LD + at + 4);

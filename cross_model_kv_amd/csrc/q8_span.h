@@ -44,6 +44,15 @@ KVMAP_HD Q8Span q8_span(int64_t start, int64_t count, int64_t n, int64_t j, cons
     return s;
 }
 
+// r / G by multiplication, for r < 2^28 and G <= 2^28: with 2^c >= G, mul = 2^(28 + c) / G rounded up exceeds that by less than
+// 1, so r * mul / 2^(28 + c) exceeds r / G by less than 2^28 / 2^(28 + c) <= 1 / G.
+KVMAP_HD void q8_divisor(uint32_t G, uint32_t& mul, int& shift) {
+    shift = 28;
+    while (((uint64_t)1 << (shift - 28)) < G) ++shift;
+    mul = (uint32_t)((((uint64_t)1 << shift) + G - 1) / G);
+}
+KVMAP_HD int q8_divide(int r, uint32_t mul, int shift) { return (int)((uint64_t)(uint32_t)r * mul >> shift); }
+
 // What piece w of a line of work, cut every `share` units, takes of an item whose tiles are the units at .. at + tiles: the
 // tiles [t0, t1), and where t0 is 0, the number of pieces that the item is in.
 struct Q8Cut {
