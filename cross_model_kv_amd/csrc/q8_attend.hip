@@ -62,16 +62,6 @@ __host__ __device__ constexpr int per_cu(bool bf16, int nt) { return bf16 ? (nt 
 template <bool BF16, int NT>
 constexpr bool kThird = per_cu(BF16, NT) == 3;
 
-// Sums of the lanes up to and including one's own.
-__device__ __forceinline__ uint32_t wave_scan(uint32_t x, int lane) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t y = __shfl_up(x, o);
-        if (lane >= o) x += y;
-    }
-    return x;
-}
-
 // One row and 4 dims of the waves' sums, joined.
 template <int ROWS, int LDO>
 __device__ __forceinline__ void join_waves(const float (&s_o)[kWaves][ROWS][LDO], const float (&s_ml)[kWaves][ROWS][2], int row, int d4,
@@ -91,13 +81,7 @@ __device__ __forceinline__ void join_waves(const float (&s_o)[kWaves][ROWS][LDO]
 
 // Steps of one item of each of 64 sequences, summed up to and including the lane's (at most 64 * 2^22).
 __device__ __forceinline__ uint32_t steps_upto(const Q8Attend& a, int b0, int end, int lane) {
-    return wave_scan(b0 + lane < end ? (uint32_t)q8_steps(a.len[b0 + lane], a.max_len) : 0u, lane);
-}
-// The same of the sequences first .. end - 1 in all.
-__device__ __forceinline__ uint64_t steps_between(const Q8Attend& a, int first, int end, int lane) {
-    uint64_t sum = 0;
-    for (int b0 = first; b0 < end; b0 += 64) sum += __shfl(steps_upto(a, b0, end, lane), 63);
-    return sum;
+    return wave_scan(b0 + lane < end ? (uint32_t)q8_steps(a.len[b0 + lane], a.max_len) : 0u);
 }
 
 template <bool BF16, int D, int NT>
@@ -114,8 +98,8 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
 
     // this workgroup's piece [at, stop) of the line of steps, and the sequence that it begins in
     uint32_t upto = a.B == 1 ? (uint32_t)q8_steps(a.len[0], a.max_len) : steps_upto(a, 0, a.B, lane);
-    uint64_t total = __builtin_amdgcn_readlane(upto, 63);
-    for (int b0 = 64; b0 < a.B; b0 += 64) total += __shfl(steps_upto(a, b0, a.B, lane), 63);
+    uint64_t total = lane_value(upto, 63);
+    for (int b0 = 64; b0 < a.B; b0 += 64) total += lane_value(steps_upto(a, b0, a.B, lane), 63);
     total *= items;
     uint64_t share = 1;
     if (total > gridDim.x) {
@@ -140,10 +124,10 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
             if (past) {
                 const int n = __ffsll((unsigned long long)past) - 1;
                 b = b0 + n;
-                if (n) base += (uint64_t)__shfl(upto, n - 1) * items;
+                if (n) base += (uint64_t)lane_value(upto, n - 1) * items;
                 break;
             }
-            base += (uint64_t)__shfl(upto, 63) * items;
+            base += (uint64_t)lane_value(upto, 63) * items;
             b0 += 64;
             if (b0 >= a.B) return;  // (not reached while the lengths stay as they were summed)
             upto = steps_upto(a, b0, a.B, lane);

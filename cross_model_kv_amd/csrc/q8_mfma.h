@@ -169,6 +169,31 @@ struct Query<false> : Parts3 {
     }
 };
 
+// Lane n's value, n the same in all lanes.
+__device__ __forceinline__ uint32_t lane_value(uint32_t x, int n) { return (uint32_t)__builtin_amdgcn_readlane((int)x, n); }
+__device__ __forceinline__ uint64_t lane_value(uint64_t x, int n) {
+    return (uint64_t)lane_value((uint32_t)(x >> 32), n) << 32 | lane_value((uint32_t)x, n);
+}
+
+// Sums of the lanes up to and including one's own; all 64 lanes take part.  Through registers: a step through shared memory's
+// crossbar (a shuffle) is 100 cycles of waiting, and a workgroup finds its work with four such sums.
+template <int FROM, int ROWS>
+__device__ __forceinline__ uint32_t lanes_from(uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, FROM, ROWS, 0xF, false); }
+template <int FROM, int ROWS>
+__device__ __forceinline__ uint64_t lanes_from(uint64_t x) {
+    return (uint64_t)lanes_from<FROM, ROWS>((uint32_t)(x >> 32)) << 32 | lanes_from<FROM, ROWS>((uint32_t)x);
+}
+template <class T>
+__device__ __forceinline__ T wave_scan(T x) {
+    x += lanes_from<0x111, 0xF>(x);  // 1, 2, 4, 8 lanes below, inside rows of 16 (0 where there is none)
+    x += lanes_from<0x112, 0xF>(x);
+    x += lanes_from<0x114, 0xF>(x);
+    x += lanes_from<0x118, 0xF>(x);
+    x += lanes_from<0x142, 0xA>(x);  // a row's last lane, for the odd rows
+    x += lanes_from<0x143, 0xC>(x);  // lane 31, for the rows above it
+    return x;
+}
+
 // Division with the usual case of small numbers in 32 bits.
 __device__ __forceinline__ uint64_t div64(uint64_t a, uint64_t b) {
     return (a | b) >> 32 ? a / b : (uint64_t)((uint32_t)a / (uint32_t)b);

@@ -55,15 +55,6 @@ __device__ __forceinline__ int block_tiles(const Q8Attend& a, int G, int len, in
 template <bool BF16>
 constexpr int kItemCost = BF16 ? 5 : 2;
 
-__device__ __forceinline__ uint64_t wave_scan(uint64_t x, int lane) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t y = __shfl_up((unsigned long long)x, o);
-        if (lane >= o) x += y;
-    }
-    return x;
-}
-__device__ __forceinline__ uint64_t last_lane(uint64_t x) { return __shfl((unsigned long long)x, 63); }
 // Cost of all row blocks of one head: of sequence b0 + lane (0 past the last), lanes going over the sequences or over the row
 // blocks, whichever is fewer rounds.
 __device__ __forceinline__ uint64_t head_cost(const Q8Attend& a, int G, int b0, int row_blocks, int bm, int extra, int lane) {
@@ -74,7 +65,7 @@ __device__ __forceinline__ uint64_t head_cost(const Q8Attend& a, int G, int b0, 
             const int len = a.len[b0 + i];
             uint64_t s = 0;
             for (int r0 = 0; r0 < row_blocks; r0 += 64)
-                s += last_lane(wave_scan(r0 + lane < row_blocks ? block_tiles(a, G, len, r0 + lane, bm) + extra : 0, lane));
+                s += lane_value(wave_scan<uint32_t>(r0 + lane < row_blocks ? block_tiles(a, G, len, r0 + lane, bm) + extra : 0), 63);
             if (i == lane) sum = s;
         }
     } else if (lane < n) {
@@ -91,8 +82,8 @@ struct Item {
 };
 // The line's length; `first` is what head_cost gives for the first 64 sequences.  Every lane of the wave alike.
 __device__ __forceinline__ uint64_t line_length(const Q8Attend& a, int G, int row_blocks, int bm, int extra, int lane, uint64_t first) {
-    uint64_t total = last_lane(wave_scan(first, lane));
-    for (int b0 = 64; b0 < a.B; b0 += 64) total += last_lane(wave_scan(head_cost(a, G, b0, row_blocks, bm, extra, lane), lane));
+    uint64_t total = lane_value(wave_scan(first), 63);
+    for (int b0 = 64; b0 < a.B; b0 += 64) total += lane_value(wave_scan(head_cost(a, G, b0, row_blocks, bm, extra, lane)), 63);
     return total * a.c.H;
 }
 // The item that holds the line's unit u (less than its length).
@@ -101,16 +92,16 @@ __device__ __forceinline__ Item find_item(const Q8Attend& a, int G, int row_bloc
     uint64_t base = 0, mine = first;
     int b0 = 0;
     while (true) {
-        const uint64_t upto = wave_scan(mine, lane) * a.c.H;
+        const uint64_t upto = wave_scan(mine) * a.c.H;
         const uint64_t past = __ballot(base + upto > u);
         const int n = past ? __ffsll((unsigned long long)past) - 1 : 63;
         it.b = min(b0 + n, a.B - 1);  // (past is not 0 in the end, while the lengths stay as they were summed)
         if (past || b0 + 64 >= a.B) {
-            mine = __shfl((unsigned long long)mine, n);
-            base += __shfl((unsigned long long)upto, n) - mine * a.c.H;
+            mine = lane_value(mine, n);
+            base += lane_value(upto, n) - mine * a.c.H;
             break;
         }
-        base += last_lane(upto);
+        base += lane_value(upto, 63);
         b0 += 64;
         mine = head_cost(a, G, b0, row_blocks, bm, extra, lane);
     }
@@ -118,17 +109,17 @@ __device__ __forceinline__ Item find_item(const Q8Attend& a, int G, int row_bloc
     base += (uint64_t)it.h * mine;
     const int len = a.len[it.b];
     for (int r0 = 0;; r0 += 64) {
-        const uint64_t cost = r0 + lane < row_blocks ? block_tiles(a, G, len, r0 + lane, bm) + extra : 0;
-        const uint64_t upto = wave_scan(cost, lane);
+        const uint32_t cost = r0 + lane < row_blocks ? block_tiles(a, G, len, r0 + lane, bm) + extra : 0;
+        const uint32_t upto = wave_scan(cost);
         const uint64_t past = __ballot(base + upto > u);
         if (past || r0 + 64 >= row_blocks) {
             const int n = past ? __ffsll((unsigned long long)past) - 1 : row_blocks - 1 - r0;
             it.rb = r0 + n;
-            it.cost = (int)__shfl((unsigned long long)cost, n);
-            it.at = base + __shfl((unsigned long long)upto, n) - it.cost;
+            it.cost = (int)lane_value(cost, n);
+            it.at = base + lane_value(upto, n) - it.cost;
             return it;
         }
-        base += last_lane(upto);
+        base += lane_value(upto, 63);
     }
 }
 
