@@ -159,6 +159,17 @@ __device__ __forceinline__ void rescale_page(uint8_t* dst, int kv, int lo, float
     }
 }
 
+// The bytes [from, to) of 4 tokens' codes of one dim; the others stay as they are.
+__device__ __forceinline__ void store_tokens(uint32_t* at, uint32_t w, int from, int to) {
+    if (from <= 0 && to >= 4) {
+        *at = w;
+    } else if (from < 4 && to > 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i >= from && i < to) ((uint8_t*)at)[i] = (uint8_t)(w >> (8 * i));
+    }
+}
+
 template <bool BF16, int D, int P>
 __global__ __launch_bounds__(256) void q8_write_kernel(Q8Pools c, Q8Seqs q, int n_slots, uint32_t items, int n, Q8Rows kr, Q8Rows vr,
                                                        unsigned int* __restrict__ dropped) {
@@ -246,16 +257,6 @@ __global__ __launch_bounds__(256) void q8_write_kernel(Q8Pools c, Q8Seqs q, int 
 #pragma unroll
         for (int i = 0; i < T::VEC / 4; ++i) w[p][i] = codes4(f + 4 * i, inv);
     }
-    if (lo > 0 || hi < P) {  // part of a page: its tokens' bytes alone
-#pragma unroll
-        for (int p = 0; p < T::PASSES; ++p) {
-            const int row = row0 + p;
-            if (row < lo || row >= hi) continue;
-#pragma unroll
-            for (int i = 0; i < T::VEC; ++i) dst[(col + i) * P + row] = (uint8_t)(w[p][i / 4] >> (8 * (i & 3)));
-        }
-        return;
-    }
     uint8_t* lds = (uint8_t*)turn;
 #pragma unroll
     for (int i = 0; i < T::VEC; ++i)
@@ -266,7 +267,13 @@ __global__ __launch_bounds__(256) void q8_write_kernel(Q8Pools c, Q8Seqs q, int 
     for (int i = tid; i < D * (P / 16); i += T::GROUP) {
         const int dim = i / (P / 16), k = i % (P / 16);
         const uint32_t* a = turn + dim * T::LDW + 4 * k;
-        *(uint4*)(dst + dim * P + 16 * k) = make_uint4(a[0], a[1], a[2], a[3]);
+        uint32_t* to = (uint32_t*)(dst + dim * P + 16 * k);
+        if (lo <= 16 * k && 16 * k + 16 <= hi) {
+            *(uint4*)to = make_uint4(a[0], a[1], a[2], a[3]);
+        } else {  // (byte by byte, pages of 128 tokens of which 81 enter took five times as long)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) store_tokens(to + z, a[z], lo - 16 * k - 4 * z, hi - 16 * k - 4 * z);
+        }
     }
 }
 
@@ -340,12 +347,9 @@ __global__ __launch_bounds__(256) void q8_read_kernel(Q8Pools c, Q8Seqs q, int n
     }
 }
 
-// Writes of at most kFew tokens a sequence: a wave takes a page, its lanes D / 64 dims of every row that enters, so that a
-// page's other rows cost nothing.  A token of 16 sequences in 40 layers: 13 us in bf16 pages of 64 and in fp32 ones of 128,
-// 33 and 49 in the kernel above.  Eight tokens of 4 sequences in 8 layers take 7.6 us here and 8.1 there; the lanes' loads
-// are 4 bytes, not 16, and eight rows fill their registers.
-constexpr int kFew = 8;
-template <bool BF16, int D, int P>
+// Writes of at most FEW tokens a sequence: a wave takes a page, its lanes D / 64 dims of every row that enters, so that a
+// page's other rows cost nothing.
+template <bool BF16, int D, int P, int FEW>
 __global__ __launch_bounds__(256) void q8_write_few_kernel(Q8Pools c, Q8Seqs q, int n_slots, uint32_t items, int n, Q8Rows kr, Q8Rows vr,
                                                            unsigned int* __restrict__ dropped) {
     constexpr int V = D / 64, ES = BF16 ? 2 : 4;
@@ -368,10 +372,10 @@ __global__ __launch_bounds__(256) void q8_write_few_kernel(Q8Pools c, Q8Seqs q, 
     const Q8Rows& r = it.kv ? vr : kr;
     const char* src = (const char*)r.base +
                       (it.layer * r.layer + it.b * r.seq + it.h * r.head + (sp.p0 + lo) * r.token + lane * V) * ES;
-    float x[kFew][V];
+    float x[FEW][V];
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kFew; ++i) {
+    for (int i = 0; i < FEW; ++i) {
         if (i >= rows) break;
         const char* at = src + i * r.token * ES;
         if (BF16 && V == 2) {
@@ -400,18 +404,34 @@ __global__ __launch_bounds__(256) void q8_write_few_kernel(Q8Pools c, Q8Seqs q, 
     }
     if (lane == 0) *scale_at = scale;
     const float inv = 1.f / scale;  // exact: a power of two
+    uint64_t w[FEW / 8][V] = {};  // a dim's tokens side by side
 #pragma unroll
-    for (int i = 0; i < kFew; ++i) {
+    for (int i = 0; i < FEW; ++i) {
         if (i >= rows) break;
-        float y[4] = {x[i][0], x[i][V - 1], 0.f, 0.f};
-        const uint32_t w = codes4(y, inv);
+        const float y[4] = {x[i][0], x[i][V - 1], 0.f, 0.f};
+        const uint32_t codes = codes4(y, inv);
         if (it.kv) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) dst[(lane * V + k) * P + lo + i] = (uint8_t)(w >> (8 * k));
+            for (int k = 0; k < V; ++k) w[i / 8][k] |= (uint64_t)(codes >> (8 * k) & 0xFF) << (8 * (i & 7));
         } else if (V == 2) {
-            *(uint16_t*)(dst + (lo + i) * D + 2 * lane) = (uint16_t)w;
+            *(uint16_t*)(dst + (lo + i) * D + 2 * lane) = (uint16_t)codes;
         } else {
-            dst[(lo + i) * D + lane] = (uint8_t)w;
+            dst[(lo + i) * D + lane] = (uint8_t)codes;
+        }
+    }
+    if (it.kv == 0) return;
+    const int skip = lo & 3;  // they begin in a dword's middle
+#pragma unroll
+    for (int e = 0; e < FEW / 8; ++e) {
+        const int live = rows - 8 * e + skip;
+        if (live <= skip) break;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            uint32_t* to = (uint32_t*)(dst + (lane * V + k) * P) + lo / 4 + 2 * e;
+            const uint64_t low = w[e][k] << (8 * skip);
+            store_tokens(to, (uint32_t)low, skip, live);
+            store_tokens(to + 1, (uint32_t)(low >> 32), skip - 4, live - 4);
+            if (skip && live > 8) store_tokens(to + 2, (uint32_t)(w[e][k] >> (64 - 8 * skip)), 0, min(live, 8 + skip) - 8);
         }
     }
 }
@@ -419,45 +439,68 @@ __global__ __launch_bounds__(256) void q8_write_few_kernel(Q8Pools c, Q8Seqs q, 
 // A row range of n tokens touches at most this many pages.
 int slots(int n, int page) { return (int)(((int64_t)n + 2 * page - 2) / page); }
 
+// f(Shape<bf16, d, page>()) for what a call has.
+template <bool B, int DIMS, int TOKENS>
+struct Shape {
+    static constexpr bool BF16 = B;
+    static constexpr int D = DIMS, P = TOKENS;
+};
+template <bool BF16, int D, class F>
+void with_page(int page, F&& f) {
+    if (page == 16) f(Shape<BF16, D, 16>());
+    else if (page == 32) f(Shape<BF16, D, 32>());
+    else if (page == 64) f(Shape<BF16, D, 64>());
+    else f(Shape<BF16, D, 128>());
+}
+template <class F>
+void with_shape(Elem e, const Q8Pools& c, F&& f) {
+    if (e == Elem::BF16) c.d == 128 ? with_page<true, 128>(c.page, f) : with_page<true, 64>(c.page, f);
+    else c.d == 128 ? with_page<false, 128>(c.page, f) : with_page<false, 64>(c.page, f);
+}
+
+// Workgroups for items that 256 / GROUP of them take.
+template <int GROUP>
+dim3 grid_of(uint32_t items) { return dim3((items + 256 / GROUP - 1) / (256 / GROUP)); }
+
 }  // namespace
 
-// KERNEL<bf16, d, page> over the items of a call, GROUP threads on each.
-#define KVMAP_Q8_PAGES(KERNEL, GROUP, ...)                                                                      \
-    do {                                                                                                        \
-        const int ns = slots(n, c.page);                                                                        \
-        const uint32_t items = (uint32_t)((int64_t)ns * q.B * c.H * n_layers * 2);                              \
-        if (e == Elem::BF16) {                                                                                  \
-            if (c.d == 128) KVMAP_Q8_P(KERNEL, GROUP, true, 128, __VA_ARGS__);                                  \
-            else KVMAP_Q8_P(KERNEL, GROUP, true, 64, __VA_ARGS__);                                              \
-        } else {                                                                                                \
-            if (c.d == 128) KVMAP_Q8_P(KERNEL, GROUP, false, 128, __VA_ARGS__);                                 \
-            else KVMAP_Q8_P(KERNEL, GROUP, false, 64, __VA_ARGS__);                                             \
-        }                                                                                                       \
-    } while (0)
-#define KVMAP_Q8_P(KERNEL, GROUP, B, D, ...)                                                                    \
-    do {                                                                                                        \
-        if (c.page == 16) KVMAP_Q8_L(KERNEL, GROUP, B, D, 16, __VA_ARGS__);                                     \
-        else if (c.page == 32) KVMAP_Q8_L(KERNEL, GROUP, B, D, 32, __VA_ARGS__);                                \
-        else if (c.page == 64) KVMAP_Q8_L(KERNEL, GROUP, B, D, 64, __VA_ARGS__);                                \
-        else KVMAP_Q8_L(KERNEL, GROUP, B, D, 128, __VA_ARGS__);                                                 \
-    } while (0)
-#define KVMAP_Q8_L(KERNEL, GROUP, B, D, P, ...)                                                                 \
-    hipLaunchKernelGGL((KERNEL<B, D, P>), dim3((items + 256 / GROUP(B, D, P) - 1) / (256 / GROUP(B, D, P))), dim3(256), 0, s, c, q, ns, \
-                       items, n, __VA_ARGS__)
-#define KVMAP_Q8_WRITE_GROUP(B, D, P) (WriteTile<B, D, P>::GROUP)
-#define KVMAP_Q8_READ_GROUP(B, D, P) (ReadTile<B, D, P>::GROUP)
-#define KVMAP_Q8_WAVE(B, D, P) 64
+// Which tokens are few.  One token of 16 sequences in 40 layers: 13 us by the wave (bf16 pages of 64, fp32 ones of 128), 33 and
+// 49 by the workgroup; 8 tokens of 4 sequences in 8 layers 7.2 and 7.7.  Up to 16 tokens only where there are many pages, each a
+// workgroup's, since the wave's rows come 4 bytes a lane: 16 tokens of 16 sequences in 40 layers (20,480 pages) 52 and 75 us, of
+// 8 in 16 (4,096) 16.8 and 20.0, of 8 in 8 (2,048) 12.7 and 12.2.
+constexpr int kFew = 8, kSome = 16;
+constexpr uint32_t kManyPages = 4096;
 
 hipError_t launch_q8_write(Elem e, const Q8Pools& c, const Q8Seqs& q, int n_layers, int n, const Q8Rows& k,
                            const Q8Rows& v, unsigned int* dropped, hipStream_t s) {
-    if (n <= kFew) KVMAP_Q8_PAGES(q8_write_few_kernel, KVMAP_Q8_WAVE, k, v, dropped);
-    else KVMAP_Q8_PAGES(q8_write_kernel, KVMAP_Q8_WRITE_GROUP, k, v, dropped);
+    const int ns = slots(n, c.page);
+    const uint32_t items = (uint32_t)((int64_t)ns * q.B * c.H * n_layers * 2);
+    with_shape(e, c, [&](auto shape) {
+        using S = decltype(shape);
+        constexpr int GROUP = WriteTile<S::BF16, S::D, S::P>::GROUP;
+        if (n <= kFew) {
+            hipLaunchKernelGGL((q8_write_few_kernel<S::BF16, S::D, S::P, kFew>), grid_of<64>(items), dim3(256), 0, s, c, q, ns, items, n, k, v, dropped);
+            return;
+        }
+        if constexpr (GROUP == 256)
+            if (n <= kSome && items >= kManyPages) {
+                hipLaunchKernelGGL((q8_write_few_kernel<S::BF16, S::D, S::P, kSome>), grid_of<64>(items), dim3(256), 0, s, c, q, ns, items, n, k, v, dropped);
+                return;
+            }
+        hipLaunchKernelGGL((q8_write_kernel<S::BF16, S::D, S::P>), grid_of<GROUP>(items), dim3(256), 0, s, c, q, ns, items, n, k, v, dropped);
+    });
     return hipGetLastError();
 }
 
 hipError_t launch_q8_read(Elem e, const Q8Pools& c, const Q8Seqs& q, int n_layers, int n, const Q8Rows& k,
                           const Q8Rows& v, hipStream_t s) {
-    KVMAP_Q8_PAGES(q8_read_kernel, KVMAP_Q8_READ_GROUP, k, v);
+    const int ns = slots(n, c.page);
+    const uint32_t items = (uint32_t)((int64_t)ns * q.B * c.H * n_layers * 2);
+    with_shape(e, c, [&](auto shape) {
+        using S = decltype(shape);
+        constexpr int GROUP = ReadTile<S::BF16, S::D, S::P>::GROUP;
+        hipLaunchKernelGGL((q8_read_kernel<S::BF16, S::D, S::P>), grid_of<GROUP>(items), dim3(256), 0, s, c, q, ns, items, n, k, v);
+    });
     return hipGetLastError();
 }
 

@@ -99,3 +99,26 @@ def test_few_tokens_out_of_range_are_counted(ctx, K):
     want = Q.write(o, k64, v64, table, start, count)
     _same(c, o)
     assert ctx.q8_dropped() == want > 0
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (64, 128), (128, 32), (128, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_up_to_a_small_page_of_tokens(ctx, K, d, page, dtype):
+    """Ten to seventeen tokens, beginning at every place of a dword."""
+    for n in (10, 12, 13, 15, 16, 17):
+        rng = np.random.default_rng([2026, 865, d, page, n])
+        start = [0, 1, 2, 3, page - 2, page + 5, 2 * page - n // 2]
+        count = None if n % 2 else [n, n, n, n, n, 9, n - 3]
+        _write(ctx, K, rng, 1, 7, 2, n, start, count, d, page, dtype, "heads" if n % 3 else "tokens")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_pages_that_begin_and_end_anywhere(ctx, K, d, page, dtype):
+    """Writes longer than a small page whose first and last pages are partial, at every place of 16 bytes and of a dword."""
+    for n in (18, 31, page + 1, 2 * page + 19):
+        rng = np.random.default_rng([2026, 866, d, page, n])
+        start = [0, 1, 6, 11, 15, page - 1, page + 7]
+        count = [n, n, n - 1, n, n - 2, n, n // 2]
+        _write(ctx, K, rng, 1, 7, 2, n, start, count, d, page, dtype, "heads")
