@@ -308,6 +308,7 @@ __global__ __launch_bounds__(256) void q8_read_kernel(Q8Pools c, Q8Seqs q, int n
     if (it.kv && held && live > lo) {
         for (int i = tid; i < D * (P / 16); i += T::GROUP) {
             const int dim = i / (P / 16), k = i % (P / 16);
+            if (16 * k + 16 <= lo || 16 * k >= live) continue;
             const uint4 a = *(const uint4*)(src + dim * P + 16 * k);
             uint32_t* w = turn + dim * T::LDW + 4 * k;
             w[0] = a.x;
@@ -436,6 +437,62 @@ __global__ __launch_bounds__(256) void q8_write_few_kernel(Q8Pools c, Q8Seqs q, 
     }
 }
 
+// Reads of at most FEW tokens a sequence, in the same way.
+template <bool BF16, int D, int P, int FEW>
+__global__ __launch_bounds__(256) void q8_read_few_kernel(Q8Pools c, Q8Seqs q, int n_slots, uint32_t items, int n, Q8Rows kr, Q8Rows vr) {
+    constexpr int V = D / 64, ES = BF16 ? 2 : 4;
+    const uint32_t index = blockIdx.x * 4 + wave_of_thread();
+    if (index >= items) return;
+    const Item it = item_of(index, n_slots, q.B, c.H);
+    const int lane = threadIdx.x & 63;
+    const Q8Span sp = q8_span(q.start[it.b], q.count ? q.count[it.b] : n, n, it.j, q.pages + (int64_t)it.b * q.max_pages,
+                              q.max_pages, c.n_pages, P);
+    if (sp.lo >= sp.hi) return;
+    const bool held = sp.page >= 0;
+    const int lo = sp.lo, rows = sp.hi - lo, live = sp.live - lo;  // rows [live, rows) are zeros
+    const int64_t page = it.layer * c.layer_scales + (int64_t)(held ? sp.page : 0) * c.H + it.h;
+    const uint8_t* src = (it.kv ? c.v : c.k) + page * (P * D);
+    const float scale = held ? (it.kv ? c.vs : c.ks)[page] : __uint_as_float(0x7FC00000u);
+    uint32_t codes[FEW] = {};  // of a row's V dims
+    if (held && it.kv == 0) {
+#pragma unroll
+        for (int i = 0; i < FEW; ++i)
+            if (i < live) codes[i] = V == 2 ? *(const uint16_t*)(src + (lo + i) * D + 2 * lane) : src[(lo + i) * D + lane];
+    } else if (held) {
+        const int skip = lo & 3;  // they begin in a dword's middle
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const uint32_t* from = (const uint32_t*)(src + (lane * V + k) * P) + lo / 4;
+            uint32_t w[FEW / 4 + 1] = {};
+#pragma unroll
+            for (int j = 0; j <= FEW / 4; ++j)
+                if (4 * j < skip + live) w[j] = from[j];
+#pragma unroll
+            for (int j = 0; j < FEW / 4; ++j) {
+                const uint32_t four = (uint32_t)(((uint64_t)w[j + 1] << 32 | w[j]) >> (8 * skip));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) codes[4 * j + i] |= (four >> (8 * i) & 0xFF) << (8 * k);
+            }
+        }
+    }
+    const Q8Rows& r = it.kv ? vr : kr;
+    char* out = (char*)r.base + (it.layer * r.layer + it.b * r.seq + it.h * r.head + (sp.p0 + lo) * r.token + lane * V) * ES;
+#pragma unroll
+    for (int i = 0; i < FEW; ++i) {
+        if (i >= rows) break;
+        float f[4];
+        values4(codes[i], f);
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] = i >= live ? 0.f : held ? f[k] * scale : scale;
+        char* at = out + i * r.token * ES;
+        if (BF16 && V == 2) *(uint32_t*)at = pack_bf16(f[0], f[1]);
+        else if (BF16) *(uint16_t*)at = (uint16_t)pack_bf16(f[0], 0.f);
+        else
+#pragma unroll
+            for (int k = 0; k < V; ++k) ((float*)at)[k] = f[k];
+    }
+}
+
 // A row range of n tokens touches at most this many pages.
 int slots(int n, int page) { return (int)(((int64_t)n + 2 * page - 2) / page); }
 
@@ -467,7 +524,8 @@ dim3 grid_of(uint32_t items) { return dim3((items + 256 / GROUP - 1) / (256 / GR
 // Which tokens are few.  One token of 16 sequences in 40 layers: 13 us by the wave (bf16 pages of 64, fp32 ones of 128), 33 and
 // 49 by the workgroup; 8 tokens of 4 sequences in 8 layers 7.2 and 7.7.  Up to 16 tokens only where there are many pages, each a
 // workgroup's, since the wave's rows come 4 bytes a lane: 16 tokens of 16 sequences in 40 layers (20,480 pages) 52 and 75 us, of
-// 8 in 16 (4,096) 16.8 and 20.0, of 8 in 8 (2,048) 12.7 and 12.2.
+// 8 in 16 (4,096) 16.8 and 20.0, of 8 in 8 (2,048) 12.7 and 12.2.  Reads: 8 tokens of those 16 sequences 15 and 39 us, 16 of 8 in
+// 16 layers 10.1 and 12.4.
 constexpr int kFew = 8, kSome = 16;
 constexpr uint32_t kManyPages = 4096;
 
@@ -499,6 +557,15 @@ hipError_t launch_q8_read(Elem e, const Q8Pools& c, const Q8Seqs& q, int n_layer
     with_shape(e, c, [&](auto shape) {
         using S = decltype(shape);
         constexpr int GROUP = ReadTile<S::BF16, S::D, S::P>::GROUP;
+        if (n <= kFew) {
+            hipLaunchKernelGGL((q8_read_few_kernel<S::BF16, S::D, S::P, kFew>), grid_of<64>(items), dim3(256), 0, s, c, q, ns, items, n, k, v);
+            return;
+        }
+        if constexpr (GROUP == 256)
+            if (n <= kSome && items >= kManyPages) {
+                hipLaunchKernelGGL((q8_read_few_kernel<S::BF16, S::D, S::P, kSome>), grid_of<64>(items), dim3(256), 0, s, c, q, ns, items, n, k, v);
+                return;
+            }
         hipLaunchKernelGGL((q8_read_kernel<S::BF16, S::D, S::P>), grid_of<GROUP>(items), dim3(256), 0, s, c, q, ns, items, n, k, v);
     });
     return hipGetLastError();

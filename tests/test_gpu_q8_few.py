@@ -122,3 +122,25 @@ def test_pages_that_begin_and_end_anywhere(ctx, K, d, page, dtype):
         start = [0, 1, 6, 11, 15, page - 1, page + 7]
         count = [n, n, n - 1, n, n - 2, n, n // 2]
         _write(ctx, K, rng, 1, 7, 2, n, start, count, d, page, dtype, "heads")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("n", [1, 3, 8, 13])
+def test_few_tokens_read_out_of_range(ctx, K, d, page, dtype, n):
+    """Reads where pages, starts or counts are not what they have to be: NaN there, zeros past a count, the others whole."""
+    rng = np.random.default_rng([2026, 867, d, n])
+    H, n_pages, L = 2, 6, 2
+    o = _pool(rng, L, n_pages, H, page, d)
+    c = _from_oracle(K, o)
+    table = [[0, 1], [2, n_pages], [-1, 3], [4, 5], [4, 5], [1, 0]]
+    start = [page - 2, page - 1, page - n // 2, -1, 2 * page - 1, 3]
+    for count in (None, [n, n - 1, n, n, n, n + 1]):
+        ct = None if count is None else _ints(count)
+        gk, gv = ctx.q8_read(c, _ints(table), _ints(start), n, count=ct, layer=0, n_layers=L, dtype=_dt(dtype))
+        bad = [s < 0 or m > n for s, m in zip(start, count or [n] * 6)]
+        want = Q.read(o, [t + [-1, -1] for t in table], [0 if x else s for x, s in zip(bad, start)], n,
+                      [0 if x else m for x, m in zip(bad, count or [n] * 6)], 0, L)
+        for got, ref in zip((gk, gv), want):
+            ref[:, bad] = np.nan
+            np.testing.assert_array_equal(_f64(got), ref)
