@@ -24,9 +24,9 @@
 // l = sum pv / v_scale, in 64 bits.  fp32 calls: queries and weights as three bf16 parts each (24 bits).
 //
 // What bounds it: bytes, where there are enough of them.  64 sequences of up to 16,384 tokens, 64 query and 8 KV heads: 1.08 GB
-// in 205 us, 5.2 TB/s (a copy of 4 GiB reaches 4.75); 32,768 tokens of one: 67 MB in 17.7 us and 4 to join.  Below some
-// thousand tokens a sequence it is the way through one step: 3,000 cycles until a workgroup knows its piece, 2,000 for
-// its item and queries, 5,000 to 8,000 a tile (900 instructions at 4.5 cycles, and the CU's 64 bytes a cycle), 3,000 to join the
+// in 200 us, 5.35 TB/s (a copy of 4 GiB reaches 4.75); 32,768 tokens of one: 67 MB in 17 us and 4 to join.  Below some
+// thousand tokens a sequence it is the way through one step: 2,500 cycles until a workgroup knows its piece, 6,000 to 8,500 for
+// its item, queries and a tile (900 instructions at 4.5 cycles, and the CU's 64 bytes a cycle), 2,500 to join the
 // waves and store: 7.2 us for 130 tokens.
 
 #include <algorithm>

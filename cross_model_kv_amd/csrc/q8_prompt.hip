@@ -12,8 +12,8 @@
 // What bounds it: a tile costs a SIMD (64 rows) 2054 cycles of matrix products, 2215 of issuing vector instructions
 // (these among them) and takes 4090; the clock meanwhile falls to 1.6 - 1.8 GHz.  Waves of 64 rows, one a SIMD, read
 // half as much shared memory but cannot issue fast enough (an instruction every 5 cycles, 580 of them a tile): 4400
-// cycles at a clock as much higher, the same time within 3 %: 1.08 - 1.12 ms for 8,192 rows a head, 8 heads and 33,792 tokens
-// (1000 - 1030 TFLOP/s, against 1430 - 1550 of large library products here).  Products next to the vector work in the order
+// cycles at a clock as much higher, the same time within 3 %: 1.06 - 1.15 ms by box for 8,192 rows a head, 8 heads and 33,792 tokens
+// (970 - 1050 TFLOP/s, against 1430 - 1550 of large library products here).  Products next to the vector work in the order
 // in which they are written, not the compiler's, took waves of 64 rows from 1470 us to 1220 - 1300.
 
 #include <algorithm>
