@@ -138,8 +138,14 @@ __device__ __forceinline__ void wave_memory() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Workgroups that a CU holds at once.  bf16 with 128 dims: one of 8 waves, or two of 4, which have shared memory for two tiles of
+// keys each, not three, and so a barrier more a tile.  (One of 4 waves and three tiles: 64 rows of 8 sequences of 8,192 tokens 62 us
+// for 54.8, of one of 32,768 37.7 for 35.0.)
 template <bool BF16, int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q8_prompt_kernel(Q8Attend a, Q8Pieces sp) {
+constexpr int kPerCu = D == 64 || (BF16 && WAVES == 4) ? 2 : 1;
+
+template <bool BF16, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) void q8_prompt_kernel(Q8Attend a, Q8Pieces sp) {
     constexpr int BM = 32 * WAVES;             // rows of a workgroup
     constexpr int KROW = 2 * D + 16;           // bytes of a token's keys in shared memory: the 16 spread the banks
     constexpr int KBYTES = kTile * KROW;
@@ -149,8 +155,9 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
     constexpr int NQ = D / 8, NV = D / 8;      // operands of a tile: keys, values
     constexpr int AHEAD = 3;
     constexpr int CPT = D / 16;                // such loads of a token's keys
-    __shared__ __align__(16) uint8_t s_k[3 * KBYTES + 2 * D * VROW];
-    uint8_t* const s_v = s_k + 3 * KBYTES;
+    constexpr int RING = D == 128 && kPerCu<BF16, D, WAVES> == 2 ? 2 : 3;  // tiles of keys
+    __shared__ __align__(16) uint8_t s_k[RING * KBYTES + 2 * D * VROW];
+    uint8_t* const s_v = s_k + RING * KBYTES;
     __shared__ int s_nan;                      // some value was taken out
     __shared__ float2 s_scale[4][4];           // k_scale, v_scale of 16 tokens each; a tile's are written with its keys
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -285,7 +292,7 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
         float cs, bias;        // its scales, made of
         float2 scl;
         int ev;                // the value scale's exponent
-        int k_at = 0, k_next = KBYTES, k_last = 2 * KBYTES;  // where tiles t, t + 1, t + 2 keep their keys
+        int k_at = 0, k_next = KBYTES, k_last = RING == 3 ? 2 * KBYTES : 0;  // where tiles t, t + 1, t + 2 keep their keys
         auto read_scale = [&](int tile, int mt) { scl = s_scale[tile & 3][2 * mt + hi]; };
         auto use_scale = [&]() {
             ev = scale_exponent(scl.y);
@@ -454,12 +461,13 @@ __global__ __launch_bounds__(64 * WAVES, (D == 64 || WAVES == 8 ? 2 : 1)) void q
         for (int tile = t0; tile < t1; ++tile) {
             step(std::integral_constant<int, 0>{}, tile, even, odd);
             settle(std::false_type{}, tile, 1, odd);
+            if constexpr (RING == 2) __syncthreads();  // no wave reads this tile's keys any more: tile + 2's come there
             step(std::integral_constant<int, 1>{}, tile, odd, even);
             store_scale(tile + 2, sc, pv);
             const int k = k_at;
             k_at = k_next;
-            k_next = k_last;
-            k_last = k;
+            k_next = RING == 3 ? k_last : k;
+            k_last = RING == 3 ? k : k_at;
             __syncthreads();
             if (tile + 1 < t1) settle(std::false_type{}, tile + 1, 0, even);
         }
@@ -586,7 +594,11 @@ Q8Plan q8_prompt_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len,
     p.prompt = true;
     p.rows = bf16 && d == 128 && R > 128 ? 256 : 128;
     p.row_blocks = (int)((R + p.rows - 1) / p.rows);
-    const int tiles = std::max(1, (max_len + kTile - 1) / kTile), per_cu = d == 64 ? 2 : 1;
+    const int tiles = std::max(1, (max_len + kTile - 1) / kTile);
+    // Two workgroups of 4 waves from 16 tiles a CU on (below, the pieces are so short that joining more of them costs more): 64 rows
+    // of 4 sequences of 4,000 tokens with 8 heads are 8 a CU, and take 27 us by one workgroup a CU, 29 by two.
+    const double work = (double)B * H * p.row_blocks * (tiles + kItemCost<true>);
+    const int per_cu = d == 64 || (bf16 && p.rows == 128 && work >= 16.0 * cus) ? 2 : 1;
     p.grid = (int)std::min<double>((double)per_cu * cus, (double)B * H * p.row_blocks * tiles);
     p.splits = p.grid > 1 && tiles > 1;
     return p;
