@@ -12,7 +12,7 @@
 // What bounds it: a tile costs a SIMD (64 rows) 2054 cycles of matrix products, 2215 of issuing vector instructions
 // (these among them) and takes 4090; the clock meanwhile falls to 1.6 - 1.8 GHz.  Waves of 64 rows, one a SIMD, read
 // half as much shared memory but cannot issue fast enough (an instruction every 5 cycles, 580 of them a tile): 4400
-// cycles at a clock as much higher, the same time within 3 %: 1.06 - 1.15 ms by box for 8,192 rows a head, 8 heads and 33,792 tokens
+// cycles at a clock as much higher, the same time within 3 %: 1.06 - 1.15 ms by card for 8,192 rows a head, 8 heads and 33,792 tokens
 // (970 - 1050 TFLOP/s, against 1430 - 1550 of large library products here).  Products next to the vector work in the order
 // in which they are written, not the compiler's, took waves of 64 rows from 1470 us to 1220 - 1300.
 
@@ -582,8 +582,9 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
 
 }  // namespace
 
-// More rows of a sequence and KV head than this take this kernel.  (40, 48 and 64 rows of 16 sequences of up to 3,000 tokens:
-// 36.9, 62 (fp32, 8 heads) and 37.6 us here, 38.5, 79 and 42 in q8_attend.hip's; 24 and 32 rows: 35 here, 27 and 28 there.)
+// More rows of a sequence and KV head than this take this kernel.  (48 rows in fp32 and 64 in bf16 of 16 sequences of up to 3,000
+// tokens with 8 heads: 63 and 34 us here, 79 and 42 in a kernel like q8_attend.hip's with three and four row tiles; 24 and 32 rows:
+// 35 here, 26 and 27 there.)
 constexpr int64_t kPromptRows = 32;
 
 Q8Plan q8_prompt_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus) {
