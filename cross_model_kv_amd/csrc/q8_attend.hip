@@ -17,11 +17,13 @@
 // a dim that the lane's load of the (dim-major) values brings.  Keys are read as 16 adjacent dims of a
 // token.  No shared memory and no barrier in the loop.
 //
-// 8 bits to 16: a code is exact in bf16 and in fp16, so scales stay out of the operands: the key's goes into
-// the score, the value's into the weight.  bf16 calls: bf16 queries; weights in fp16 (11 bits; bf16's 8 would
-// cost the output as much as its own rounding does).  Weights are held as pv = exp2(y2 + log2 v_scale - m) with m
-// the running maximum of that exponent, so pv stays in fp16's range whatever the scales are, and
-// l = sum pv / v_scale, in 64 bits.  fp32 calls: queries and weights as three bf16 parts each (24 bits).
+// 8 bits to 16: a code is exact in bf16, so scales stay out of the operands: the key's goes into the score, the value's into the
+// weight, pv = exp2(y2 + log2 v_scale - m) with m the running maximum of that exponent, and l = sum pv / v_scale, in 64 bits.  bf16
+// calls: bf16 queries, weights as two bf16 parts (16 bits).  fp32 calls: queries and weights as three (24 bits).  Parts have fp32's
+// exponents, so a weight counts however far below the row's largest it lies; in fp16, 11 bits in one part, weights under 2^-24 are
+// gone, and they are the whole answer of a row whose weight lies on tokens with values of zero.  (The second part costs a step of 32,768
+// tokens of one sequence 2 %, 21.0 -> 21.5 us, 64 sequences of up to 16,384 1 %, 202.6 -> 204, 4 drafted tokens of 16 sequences of up to
+// 5,003 5 %, 19.5 -> 20.6.)
 //
 // What bounds it: bytes, where there are enough of them.  64 sequences of up to 16,384 tokens, 64 query and 8 KV heads: 1.08 GB
 // in 200 us, 5.35 TB/s (a copy of 4 GiB reaches 4.75); 32,768 tokens of one: 67 MB in 17 us and 4 to join.  Below some
@@ -56,6 +58,9 @@ struct TileData {
 // stops at two row tiles and a test reads every instance's scratch size.
 template <bool BF16, int D, int NT>
 constexpr int kOccupancy = BF16 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 2 : 1);
+
+template <bool BF16>
+using RowWeights = PartWeights<BF16 ? 2 : 3>;
 
 // Workgroups that a CU holds at once, as the registers (kOccupancy) and the shared memory allow.
 __host__ __device__ constexpr int per_cu(bool bf16, int nt) { return bf16 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 2 : 1); }
@@ -268,7 +273,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
                     for (int d = 0; d < D / 16; ++d) o[n][d] *= keep;
                 }
             }
-            Weights<BF16> w[NT][2];
+            RowWeights<BF16> w[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float pv[16];
@@ -305,8 +310,8 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) {
-                const auto v0 = Weights<BF16>::codes(x.v[t][0], x.v[t][1]);
-                const auto v1 = Weights<BF16>::codes(x.v[t][2], x.v[t][3]);
+                const auto v0 = RowWeights<BF16>::codes(x.v[t][0], x.v[t][1]);
+                const auto v1 = RowWeights<BF16>::codes(x.v[t][2], x.v[t][3]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     o[n][t] = w[n][0].times(v0, o[n][t]);
@@ -342,9 +347,9 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
                             float f[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) f[e] = tok + 8 * half + e < min(end[n], len) ? 1.f : 0.f;
-                            Weights<BF16> sees;
+                            RowWeights<BF16> sees;
                             sees.set(f);
-                            hits = sees.times(Weights<BF16>::codes(is[2 * half], is[2 * half + 1]), hits);
+                            hits = sees.times(RowWeights<BF16>::codes(is[2 * half], is[2 * half + 1]), hits);
                         }
 #pragma unroll
                         for (int tt = 0; tt < D / 16; ++tt)

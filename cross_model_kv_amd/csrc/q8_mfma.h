@@ -43,12 +43,13 @@ __device__ __forceinline__ f16x8_t f16_codes(uint32_t a, uint32_t b) {
     return f16x8_t{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
 }
 
-// x as a sum of three bf16 parts (8 bits each), exact to 2^-24
-struct Parts3 {
-    bf16x8_t p[3];
+// x as a sum of N bf16 parts of 8 bits each: off by at most 2^(-8 N) of itself, over fp32's range of exponents
+template <int N>
+struct Parts {
+    bf16x8_t p[N];
     __device__ __forceinline__ void put(int i, float x0, float x1) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
+        for (int k = 0; k < N; ++k) {
             const bf16x2_t y = __builtin_convertvector((f32x2_t{x0, x1}), bf16x2_t);
             p[k][i] = y[0];
             p[k][i + 1] = y[1];
@@ -59,6 +60,23 @@ struct Parts3 {
     __device__ __forceinline__ void set(const float* x) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) put(i, x[i], x[i + 1]);
+    }
+};
+
+// Weights in N bf16 parts.
+template <int N>
+struct PartWeights : Parts<N> {
+    using Codes = bf16x8_t;
+    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b) { return bf16_codes(a, b); }
+    __device__ __forceinline__ f32x4_t times(Codes v, f32x4_t o) const {
+#pragma unroll
+        for (int k = N; k--;) o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, this->p[k], o, 0, 0, 0);
+        return o;
+    }
+    __device__ __forceinline__ f32x16_t times(Codes v, f32x16_t o) const {
+#pragma unroll
+        for (int k = N; k--;) o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, this->p[k], o, 0, 0, 0);
+        return o;
     }
 };
 
@@ -76,24 +94,10 @@ struct Weights<true> {
         for (int i = 0; i < 8; i += 2) put(i, x[i], x[i + 1]);
     }
     __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b) { return f16_codes(a, b); }
-    __device__ __forceinline__ f32x4_t times(Codes v, f32x4_t o) const { return __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p, o, 0, 0, 0); }
     __device__ __forceinline__ f32x16_t times(Codes v, f32x16_t o) const { return __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p, o, 0, 0, 0); }
 };
 template <>
-struct Weights<false> : Parts3 {
-    using Codes = bf16x8_t;
-    __device__ static __forceinline__ Codes codes(uint32_t a, uint32_t b) { return bf16_codes(a, b); }
-    __device__ __forceinline__ f32x4_t times(Codes v, f32x4_t o) const {
-        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[2], o, 0, 0, 0);
-        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[1], o, 0, 0, 0);
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[0], o, 0, 0, 0);
-    }
-    __device__ __forceinline__ f32x16_t times(Codes v, f32x16_t o) const {
-        o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[2], o, 0, 0, 0);
-        o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[1], o, 0, 0, 0);
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[0], o, 0, 0, 0);
-    }
-};
+struct Weights<false> : PartWeights<3> {};
 
 // s (+)= k q with s in vector registers and q in accumulation registers.  Where a kernel may use accumulation registers the
 // compiler puts every product's result there, and moves what vector instructions need of it, one register an instruction:
@@ -140,7 +144,7 @@ struct Query<true> {
     __device__ __forceinline__ void to_vector(bf16x8_t k, f32x16_t& s) const { mfma_to_vector<FIRST>(k, p, s); }
 };
 template <>
-struct Query<false> : Parts3 {
+struct Query<false> : Parts<3> {
     __device__ __forceinline__ void load(const void* base, int64_t at) {
         const float4 a = ((const float4*)((const float*)base + at))[0], b = ((const float4*)((const float*)base + at))[1];
         const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
