@@ -12,7 +12,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3.4028235e38f;  // the running maximum of a row that has seen no token
-constexpr float kSlack = 14.f;   // m is moved when a score passes it by more than this: weights reach 2^14, fp16 65504
+constexpr float kSlack = 14.f;   // m is moved when a score passes it by more than this (not the prompt kernel's fp16 weights)
 
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -126,6 +126,24 @@ __device__ __forceinline__ void scale_product(f32x16_t& o, float by) {
         float x = o[i], t;
         asm volatile("v_accvgpr_read_b32 %1, %0\n\tv_mul_f32 %1, %2, %1\n\tv_accvgpr_write_b32 %0, %1" : "+a"(x), "=&v"(t) : "v"(by));
         o[i] = x;
+    }
+}
+
+// x (+)= v w, and o = keep o + by x, in the same way.
+__device__ __forceinline__ void first_product(f16x8_t v, f16x8_t w, f32x16_t& x) {
+    asm volatile("s_nop 15\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, 0" : "=&v"(x) : "v"(v), "v"(w));
+}
+__device__ __forceinline__ void next_product(f16x8_t v, f16x8_t w, f32x16_t& x) {
+    asm volatile("s_nop 15\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0\n\ts_nop 15" : "+v"(x) : "v"(v), "v"(w));
+}
+__device__ __forceinline__ void add_product(f32x16_t& o, float keep, f32x16_t x, float by) {
+    asm volatile("s_nop 15" : "+a"(o));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float y = o[i], t;
+        asm volatile("v_accvgpr_read_b32 %1, %0\n\tv_mul_f32 %1, %4, %1\n\tv_fmac_f32 %1, %3, %2\n\tv_accvgpr_write_b32 %0, %1"
+                     : "+a"(y), "=&v"(t) : "v"(x[i]), "s"(by), "v"(keep));
+        o[i] = y;
     }
 }
 

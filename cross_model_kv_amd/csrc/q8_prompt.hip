@@ -38,6 +38,18 @@ __device__ __forceinline__ void each(F&& f) {
 }
 
 constexpr int kTile = 64;
+
+// The weights of bf16 calls are fp16, 2^(y - m): 11 bits from 2^-14 to 2^kTop, fewer below, one at 2^-24.  A row may have nearly all
+// of its weight on a few tokens whose values are zero, and is made of the others then, however far below those they lie;
+// so m follows the scores, up and down, and what fp16 does not hold is not lost.  Where 16 tokens' largest weight is not inside
+// 2^kDrop .. 2^kTop, m moves to the middle of the half tile's scores; there, and where a weight is below 2^kThin, what the rounding
+// takes of the weights below 2^-14 is multiplied on its own, 2^38 times as large (11 bits down to 2^-52).  Scores of a few
+// binades' spread, as 1,024 queries on 33,792 tokens have them, bring this about in one of 1,000 halves; looking for it costs the
+// call 3 % (1,145 -> 1,180 us).  With m at the largest score and no more than that, a row that had 0.9999
+// of its weight on one token lost all of its answer.
+constexpr float kTop = 15.f, kDrop = -11.f, kThin = -24.f;
+constexpr float kLift = 11.f;  // (the middle of scores further apart than fp16 reaches: m is put this far below the largest)
+constexpr float kDeep = 60.f;  // m at most this far below where it has been: 2^60 times 2^15 times 2^30 tokens' codes stays finite
 #define STEP() __builtin_amdgcn_sched_barrier(0)
 
 // Tokens that the last row of a row block sees, and its tiles: one at least, so that its rows are answered.
@@ -288,7 +300,7 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
         // The walk goes by halves of a tile, 32 tokens: half 2 t + mt is tokens 32 mt .. of tile t.  Scores of a half: token
         // 16 hi + i in x[n][i].
         f32x16_t even, odd;    // of the halves 2 t and 2 t + 1
-        float top;             // the largest of the half that comes next
+        float top, bottom;     // the largest and the smallest of the half that comes next
         float cs, bias;        // its scales, made of
         float2 scl;
         int ev;                // the value scale's exponent
@@ -303,7 +315,7 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
         // page table.
         Query<BF16> q[D / 16];
         f32x16_t o[D / 32];
-        float m = kNone;
+        float m = kNone, highest = kNone;
         double l = 0.0;
         {
             int pk1[NC];
@@ -347,30 +359,72 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
         }
         __syncthreads();
 
-        // The mask, where some row of the wave does not see all of the half; and the maximum moved where a score passes it by more
-        // than kSlack.
+        // Operands read ahead, keys of a tile at `at`.
+        u32x4_t op[AHEAD + 1];
+        const uint8_t* lane_k = s_k + c * KROW + 16 * hi;
+        const uint8_t* lane_v = s_v + c * VROW + 32 * hi;
+        auto fetch_k = [&](auto U, int at, int mt) { op[U % (AHEAD + 1)] = *(const u32x4_t*)(lane_k + at + 32 * mt * KROW + 32 * U); };
+
+        // The mask, where some row of the wave does not see all of the half; m moved; and what fp16 does not hold of weights added.
         auto settle = [&](auto FIRST, int tile, int mt, f32x16_t& x) {
             const int from = tile * kTile + 32 * mt;
             if (from + 32 > wave_end) {
                 const int see = end - from - 16 * hi;
                 top = -inf32();
+                bottom = inf32();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    x[i] = i < see ? fmaf(x[i], cs, bias) : -inf32();
+                    const float y = fmaf(x[i], cs, bias);
+                    x[i] = i < see ? y : -inf32();
                     top = fmaxf(top, x[i]);
+                    if (BF16) bottom = fminf(bottom, i < see ? y : inf32());
                 }
+                if (BF16) top = top > -inf32() ? top : m;  // (a half that is hidden moves nothing)
                 cs = 1.f;
                 bias = 0.f;
             }
-            float t = fmaf(top, cs, bias);
-            if (__any(t > m + kSlack)) {
-                t = fmaxf(fmaxf(t, __shfl_xor(t, 32)), m);
-                const float keep = __builtin_amdgcn_exp2f(m - t);
-                m = t;
-                if constexpr (!FIRST) {  // (nothing is summed yet)
-                    l *= keep;
+            const float off = bias - m;
+            float t = fmaf(top, cs, off);  // relative to m, as the weights are
+            if (!BF16) {
+                if (__any(t > kSlack)) {
+                    t = fmaxf(fmaxf(t, __shfl_xor(t, 32)), 0.f) + m;
+                    const float keep = __builtin_amdgcn_exp2f(m - t);
+                    m = t;
+                    if constexpr (!FIRST) {  // (nothing is summed yet)
+                        l *= keep;
 #pragma unroll
-                    for (int d = 0; d < D / 32; ++d) scale_product(o[d], keep);
+                        for (int d = 0; d < D / 32; ++d) scale_product(o[d], keep);
+                    }
+                }
+            } else if (__any(fabsf(t - (kTop + kDrop) / 2) > (kTop - kDrop) / 2 || fmaf(bottom, cs, off) < kThin)) {
+                t = fmaf(top, cs, bias);
+                float low = fmaf(bottom, cs, bias);
+                t = fmaxf(t, __shfl_xor(t, 32));
+                low = fminf(low, __shfl_xor(low, 32));
+                const float to = t > m + kTop || t < m + kDrop ? fmaxf(fmaxf(0.5f * t + 0.5f * low - (kTop + kThin) / 2, t - kLift), highest - kDeep) : m;
+                highest = fmaxf(highest, to);
+                const float keep = __builtin_amdgcn_exp2f(m - to);
+                m = to;
+                if constexpr (!FIRST) l *= keep;  // (else nothing is summed yet)
+                if (!FIRST || __any(low < m + kThin)) {
+                    float shift = bias - m;
+                    asm volatile("" : "+v"(shift));  // (or the compiler makes the step's weights here, ahead of its products)
+                    const uint8_t* from_v = s_v + (32 * hi + (tile & 1) * (D * VROW) + 64 * mt);
+                    f16x8_t rest[2];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float p = __builtin_amdgcn_exp2f(fmaf(x[i], cs, shift));
+                        rest[i / 8][i % 8] = (_Float16)(p < 0x1p-14f ? (p - (float)(_Float16)p) * 0x1p38f : 0.f);
+                    }
+                    each<D / 32>([&](auto I) {
+                        const f16x8_t* v = (const f16x8_t*)(from_v + (c + 32 * I) * VROW);
+                        f32x16_t sum;
+                        first_product(v[0], rest[0], sum);
+                        STEP();
+                        next_product(v[1], rest[1], sum);
+                        add_product(o[I], FIRST ? 1.f : keep, sum, 0x1p-38f);
+                        STEP();
+                    });
                 }
             }
         };
@@ -382,18 +436,18 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
         });
         product_done(even);
         top = -inf32();
+        bottom = inf32();
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) top = fmaxf(fmaxf(even[i], even[i + 1]), top);
+        for (int i = 0; i < 16; i += 2) {
+            top = fmaxf(fmaxf(even[i], even[i + 1]), top);
+            if (BF16) bottom = fminf(fminf(even[i], even[i + 1]), bottom);
+        }
         read_scale(t0, 0);
         use_scale();
 
         // A step: one half's weights and sums, and the next one's scores, instruction by instruction.  Operand u of its products is
         // read from shared memory AHEAD operands before its use, and behind every product comes the vector work that fits
         // into its time (left to itself the compiler puts the products in one heap and the exponentials in another).
-        u32x4_t op[AHEAD + 1];
-        const uint8_t* lane_k = s_k + c * KROW + 16 * hi;
-        const uint8_t* lane_v = s_v + c * VROW + 32 * hi;
-        auto fetch_k = [&](auto U, int at, int mt) { op[U % (AHEAD + 1)] = *(const u32x4_t*)(lane_k + at + 32 * mt * KROW + 32 * U); };
         auto step = [&](auto MT, int tile, const f32x16_t& s, f32x16_t& next) {
             constexpr int mt = MT, NP = (NQ + NV) / 2, E = 16;  // products, and weights of a lane
             const uint8_t* from_v = lane_v + (tile & 1) * (D * VROW) + 64 * mt;
@@ -401,6 +455,7 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
             float sum[2], p[2];
             const float shift = bias - m;
             top = -inf32();
+            bottom = inf32();
             // Weight x of the lane's 16 tokens; what is made of x - 2 and x - 1 comes with x, when they are there.
             auto weight = [&](auto X) {
                 constexpr int x = X;
@@ -416,6 +471,10 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
             auto largest = [&](auto X) {
                 top = fmaxf(fmaxf(next[2 * X], next[2 * X + 1]), top);
                 asm volatile("" : "+v"(top));  // (the same)
+                if constexpr (BF16) {
+                    bottom = fminf(fminf(next[2 * X], next[2 * X + 1]), bottom);
+                    asm volatile("" : "+v"(bottom));
+                }
             };
             each<NP>([&](auto F) {
                 constexpr int f = F, ahead = f + AHEAD;
@@ -456,8 +515,8 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
                 STEP();
             });
         };
-        each<AHEAD>([&](auto U) { fetch_k(U, k_at, 1); });
         settle(std::true_type{}, t0, 0, even);
+        each<AHEAD>([&](auto U) { fetch_k(U, k_at, 1); });
         for (int tile = t0; tile < t1; ++tile) {
             step(std::integral_constant<int, 0>{}, tile, even, odd);
             settle(std::false_type{}, tile, 1, odd);

@@ -4,8 +4,8 @@ the answer is made of the others, however far below they lie.
 
 The bound on an output element, with w the weights and A = sum_t w_t |v_t| of its row and dim (a token with a value of zero adds
 nothing to A, so A is of the answer's size here, whatever share of the weight such tokens have): the output's own rounding
-u |ref|, and A times a weight's relative error and those of its score and of the sums (test_gpu_q8.py).  A weight keeps 8 bits at
-least wherever it counts, so its error is 2^-8; in fp32 calls it keeps 24.  There is no absolute term."""
+u |ref|, and A times a weight's relative error and those of its score and of the sums (test_gpu_q8.py).  A weight in fewer bits than 8
+would show here, where it counts as the largest do elsewhere: 2^-8; in fp32 calls it keeps 24.  There is no absolute term."""
 
 import numpy as np
 import pytest
@@ -40,7 +40,8 @@ def _bounds(out, lse, ref, T, d, dtype, where):
 
 
 # Kernels by their rows of a KV head: decode's two, the prompt's of 128 rows and of 256.
-SHAPES = [(1, 8, 128, 64, "bf16"), (3, 8, 128, 32, "bf16"), (2, 8, 64, 16, "bf16"), (1, 8, 128, 64, "f32"), (40, 2, 128, 64, "f32")]
+SHAPES = [(1, 8, 128, 64, "bf16"), (3, 8, 128, 32, "bf16"), (2, 8, 64, 16, "bf16"), (30, 4, 128, 64, "bf16"), (40, 8, 128, 16, "bf16"),
+          (50, 3, 64, 128, "bf16"), (1, 8, 128, 64, "f32"), (40, 2, 128, 64, "f32")]
 
 
 def _case(rng, T, n_q, H, G, d, page, dtype, levels, zeros):
@@ -102,6 +103,19 @@ def test_stretches_at_levels_of_their_own(ctx, n_q, G, d, page, dtype):
     zeros = [(np.flatnonzero(np.arange(d) % parts != i), np.flatnonzero(part == i)) for i in range(parts)]
     o, table, q = _case(rng, T, n_q, 1, G, d, page, dtype, levels, zeros)
     _run(ctx, o, table, q, T, d, dtype, f"stretches, n_q {n_q} G {G} d {d} page {page} {dtype}")
+
+
+@pytest.mark.parametrize("n_q,G,d,page,dtype", SHAPES)
+@pytest.mark.parametrize("nats", [9, 11, 12.1, 12.7, 13.3, 17, 40])
+def test_equal_scores_far_below_the_first_ones(ctx, nats, n_q, G, d, page, dtype):
+    """After 96 tokens with values of zero, all scores are equal: a rounding of their weights would be the same for all of them."""
+    T = 1000
+    rng = np.random.default_rng([2026, 875, int(10 * nats), n_q, G, d, page])
+    levels = np.full(T, -float(nats))
+    levels[:96] = 0
+    o, table, q = _case(rng, T, n_q, 2, G, d, page, dtype, levels, [(slice(None), np.arange(96))])
+    q[..., 1:] = 0
+    _run(ctx, o, table, q, T, d, dtype, f"equal scores {nats} nats below, n_q {n_q} G {G} d {d} page {page} {dtype}")
 
 
 @pytest.mark.parametrize("n_q,G,d,page,dtype", SHAPES)
