@@ -155,7 +155,6 @@ struct Query<true> {
     __device__ __forceinline__ void load(const void* base, int64_t at) { p = *(const bf16x8_t*)((const __bf16*)base + at); }
     __device__ __forceinline__ void zero() { p = bf16x8_t{}; }
     __device__ __forceinline__ f32x4_t times(bf16x8_t k, f32x4_t s) const { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, p, s, 0, 0, 0); }
-    __device__ __forceinline__ f32x16_t times(bf16x8_t k, f32x16_t s) const { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, p, s, 0, 0, 0); }
     __device__ __forceinline__ void keep() { keep_accumulated(p); }
     // s (+)= k times the queries, s in vector registers.
     template <bool FIRST>
@@ -173,11 +172,6 @@ struct Query<false> : Parts<3> {
         s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, p[2], s, 0, 0, 0);
         s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, p[1], s, 0, 0, 0);
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, p[0], s, 0, 0, 0);
-    }
-    __device__ __forceinline__ f32x16_t times(bf16x8_t k, f32x16_t s) const {
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, p[2], s, 0, 0, 0);
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, p[1], s, 0, 0, 0);
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, p[0], s, 0, 0, 0);
     }
     __device__ __forceinline__ void keep() {
 #pragma unroll
