@@ -593,7 +593,8 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
         }
 
         // Rows that see a NaN value taken out above: which dims of which rows is the product of where the NaNs are
-        // with what the rows see.  What is NaN of what this thread has just stored becomes it.
+        // with what the rows see.  Other lanes of the wave have stored those elements (the rows were turned); the NaN goes over
+        // them, and the barrier in front of it keeps that order.
         if (__any(hidden_nan != 0)) s_nan = 1;
         __syncthreads();
         if (s_nan) {
