@@ -492,9 +492,9 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
                 // the weights, all of them by the last quarter of the products, which is what the second half of them is for
                 constexpr int e0 = std::min(f * 4 * (E + 1) / (3 * NP), E + 1), e1 = std::min((f + 1) * 4 * (E + 1) / (3 * NP), E + 1);
                 each<e1 - e0>([&](auto I) { weight(std::integral_constant<int, e0 + I>{}); });
-                // the next half's largest scores, from a little after its last product on
+                // the next half's largest and smallest scores, from a little after its last product on
                 constexpr int first = NP / 2 + (NP >= 16 ? 3 : 2), span = NP - first;
-                if constexpr (f == first && NP < 16) product_done(next);
+                if constexpr (f == first && NP < 16) product_done(next);  // (with 128 dims three products are issued between)
                 if constexpr (f >= first) {
                     constexpr int g0 = (f - first) * (E / 2) / span, g1 = (f - first + 1) * (E / 2) / span;
                     each<g1 - g0>([&](auto I) { largest(std::integral_constant<int, g0 + I>{}); });
