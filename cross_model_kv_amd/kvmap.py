@@ -354,6 +354,14 @@ class GramState:
         return int(self.c.n)
 
 
+def _made_on(stream, make):
+    """make(), whose tensors belong to `stream` (the current one if None): memory of another stream's may still be in use there."""
+    if stream is None:
+        return make()
+    with _torch().cuda.stream(stream):
+        return make()
+
+
 class Q8Cache:
     """A cache in 8 bits (kvmap_q8_cache) over the caller's device tensors:
     k [L][n_pages][H][page][d] and v [L][n_pages][H][d][page] torch.float8_e4m3fn, k_scale and v_scale
@@ -548,16 +556,17 @@ class Context:
     def q8_read(self, cache: Q8Cache, pages, start, n: int, count=None, layer: int = 0, n_layers: int | None = None,
                 dtype=None, out_k=None, out_v=None, stream=None):
         """kvmap_q8_read: (k, v) [n_layers][B][H][n][d], the n tokens from start[b] of every sequence, zeros past
-        count[b].  n_layers defaults to the layers from `layer` on; dtype (bf16 by default) to out_k's."""
+        count[b].  n_layers defaults to the layers from `layer` on; dtype (bf16 by default) to out_k's.  What the call allocates
+        belongs to `stream`."""
         torch = _torch()
         L = cache.L - layer if n_layers is None else n_layers
         if dtype is None:
             dtype = out_k.dtype if out_k is not None else torch.bfloat16
         shape = (L, pages.shape[0], cache.H, n, cache.d)
         if out_k is None:
-            out_k = torch.empty(shape, dtype=dtype, device=cache.k.device)
+            out_k = _made_on(stream, lambda: torch.empty(shape, dtype=dtype, device=cache.k.device))
         if out_v is None:
-            out_v = torch.empty_like(out_k, memory_format=torch.contiguous_format)
+            out_v = _made_on(stream, lambda: torch.empty_like(out_k, memory_format=torch.contiguous_format))
         if out_k.dtype != dtype or out_v.dtype != dtype:
             raise TypeError("out_k and out_v must be of the dtype asked for")
         self._q8_rows(lib().kvmap_q8_read, cache, out_k, out_v, pages, start, n, count, layer, _dtype_code(out_k), stream)
@@ -579,7 +588,7 @@ class Context:
         fp32, any strides of whole 16 bytes over a contiguous head dim), over layer `layer` of the cache.  pages
         [B][max_pages] and lens [B] are device int32; max_len (host) bounds the lengths; scale defaults to
         d^-1/2.  Returns out (allocated if not given), or (out, lse) where lse is a float32 [B][n_q][H_q]
-        tensor or True."""
+        tensor or True.  What the call allocates belongs to `stream`."""
         torch = _torch()
         shape = q.shape
         if len(shape) != 4 or shape[3] != cache.d:
@@ -587,7 +596,7 @@ class Context:
         B, n_q, H_q, d = shape
         max_pages = pages.shape[-1]
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out = _made_on(stream, lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
         elif out.shape != shape or out.dtype is not q.dtype:
             raise ValueError("out must match q's shape and dtype")
         if not (q.is_cuda and out.is_cuda):
@@ -602,7 +611,7 @@ class Context:
         lse_ptr = None
         if lse is not None and lse is not False:
             if lse is True:
-                lse = q.new_empty((B, n_q, H_q), dtype=torch.float32)
+                lse = _made_on(stream, lambda: q.new_empty((B, n_q, H_q), dtype=torch.float32))
             elif lse.shape != (B, n_q, H_q) or lse.dtype != torch.float32:
                 raise ValueError("lse must be float32 [B][n_q][H_q]")
             lse_ptr = _dev_ptr(lse, "lse")
