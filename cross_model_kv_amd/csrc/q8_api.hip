@@ -97,7 +97,7 @@ int check_rows(const kvmap_q8_rows* r, const char* which, int layers, int B, int
     int64_t reach = d;  // elements from the first to the last of what is covered so far
     for (auto& [stride, size] : dim) {
         if (size == 1) continue;  // never stepped
-        if (stride < 0 || (stride * (int64_t)es) % 16 || stride > kMaxElems)
+        if (stride < 0 || stride > kMaxElems || (stride * (int64_t)es) % 16)
             return report(KVMAP_ERR_INVALID_ARGUMENT, "%s: strides must be >= 0 and whole 16 bytes", which);
         if (output && stride < reach) return report(KVMAP_ERR_INVALID_ARGUMENT, "%s: output rows overlap", which);
         if ((double)stride * (double)(size - 1) > (double)kMaxElems) return report(KVMAP_ERR_SHAPE, "%s: too large", which);
