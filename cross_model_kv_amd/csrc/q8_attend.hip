@@ -26,7 +26,7 @@
 // 5,003 5 %, 19.5 -> 20.6.)
 //
 // What bounds it: bytes, where there are enough of them.  64 sequences of up to 16,384 tokens, 64 query and 8 KV heads: 1.08 GB
-// in 200 us, 5.35 TB/s (a copy of 4 GiB reaches 4.75); 32,768 tokens of one: 67 MB in 17 us and 4 to join.  Below some
+// in 197 us and 5 to join, 5.46 TB/s (a copy of 4 GiB reaches 4.75); 32,768 tokens of one: 67 MB in 18 us and 4 to join.  Below some
 // thousand tokens a sequence it is the way through one step: 2,500 cycles until a workgroup knows its piece, 6,000 to 8,500 for
 // its item, queries and a tile (900 instructions at 4.5 cycles, and the CU's 64 bytes a cycle), 2,500 to join the
 // waves and store: 7.2 us for 130 tokens.
@@ -110,8 +110,8 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
     if (total > gridDim.x) {
         share = div64(total + gridDim.x - 1, gridDim.x);
         if (kThird<BF16, NT>) {
-            // Of three workgroups a CU the third may go at once: two move 4 % more bytes a second (64 sequences of up to 16,384
-            // tokens 201 us, by three 209), and the pieces' whole steps may fit better (64 of 1,000: 34 and 40 us; 48 of
+            // Of three workgroups a CU the third may go at once: two move 3 % more bytes a second (64 sequences of up to 16,384
+            // tokens 204 us, by three 209.5), and the pieces' whole steps may fit better (64 of 1,000: 34 and 40 us; 48 of
             // 1,000: 32 and 29).
             const uint64_t two = gridDim.x - gridDim.x / 3, share2 = div64(total + two - 1, two);
             if (2 * share2 < 3 * share + share / 8) share = share2;

@@ -11,8 +11,8 @@
 // are adjacent bytes and the page is turned in LDS.  A page that a wave can hold so is a wave's, not a
 // workgroup's (bf16 pages of 16 tokens with 64 dims: 1.9 -> 4.0 to 5.2 TB/s written, 2.2 -> 5.3 read).
 //
-// Writing 8,192 mapped bf16 tokens of 64 layers with 8 heads takes 590 us, 5.45 TB/s, reading 4,096 of 40 layers 178 us,
-// 5.65 TB/s; a copy of 4 GiB reaches 4.75 TB/s.  A decode step's write (4.8 us for 64 sequences, 3.4 for one) is the launch
+// Writing 8,192 mapped bf16 tokens of 64 layers with 8 heads takes 585 us, 5.5 TB/s, reading 4,096 of 40 layers 178 us,
+// 5.65 TB/s; a copy of 4 GiB reaches 4.75 TB/s.  A decode step's write (4.7 us for 64 sequences, 3.6 for one) is the launch
 // and one page's way through memory.
 
 #include "common.h"

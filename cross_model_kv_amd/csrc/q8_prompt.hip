@@ -9,12 +9,12 @@
 // are 16 adjacent tokens, which is what P^T's operand wants of it: nothing crosses lanes, and the 16
 // tokens lie in one page, with one scale.
 //
-// What bounds it: a tile costs a SIMD (64 rows) 2054 cycles of matrix products, 2215 of issuing vector instructions
-// (these among them) and takes 4090; the clock meanwhile falls to 1.6 - 1.8 GHz.  Waves of 64 rows, one a SIMD, read
-// half as much shared memory but cannot issue fast enough (an instruction every 5 cycles, 580 of them a tile): 4400
-// cycles at a clock as much higher, the same time within 3 %: 1.06 - 1.15 ms by card for 8,192 rows a head, 8 heads and 33,792 tokens
-// (970 - 1050 TFLOP/s, against 1430 - 1550 of large library products here).  Products next to the vector work in the order
-// in which they are written, not the compiler's, took waves of 64 rows from 1470 us to 1220 - 1300.
+// What bounds it: a tile costs a SIMD (64 rows) 2050 cycles of matrix products, 2470 of issuing vector instructions
+// (these among them) and takes 4300 to 4600; the clock meanwhile falls to 1.7 - 1.9 GHz: 1.12 - 1.23 ms by card for 8,192 rows a head,
+// 8 heads and 33,792 tokens (910 - 1000 TFLOP/s, against 1430 - 1550 of large library products here).  Waves of 64 rows, one a SIMD,
+// read half as much shared memory but cannot issue fast enough (an instruction every 5 cycles, 580 of them a tile): the same
+// time within 3 %.  Products next to the vector work in the order in which they are written, not the compiler's, took waves
+// of 64 rows from 1470 us to 1220 - 1300.
 
 #include <algorithm>
 #include <utility>
@@ -151,8 +151,8 @@ __device__ __forceinline__ void wave_memory() {
 }
 
 // Workgroups that a CU holds at once.  bf16 with 128 dims: one of 8 waves, or two of 4, which have shared memory for two tiles of
-// keys each, not three, and so a barrier more a tile.  (One of 4 waves and three tiles: 64 rows of 8 sequences of 8,192 tokens 62 us
-// for 54.8, of one of 32,768 37.7 for 35.0.)
+// keys each, not three, and so a barrier more a tile.  (One of 4 waves and three tiles: 64 rows of 8 sequences of 8,192 tokens 68 us
+// for 62, of one of 32,768 39.0 for 37.3.)
 template <bool BF16, int D, int WAVES>
 constexpr int kPerCu = D == 64 || (BF16 && WAVES == 4) ? 2 : 1;
 
@@ -643,8 +643,8 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
 }  // namespace
 
 // More rows of a sequence and KV head than this take this kernel.  (48 rows in fp32 and 64 in bf16 of 16 sequences of up to 3,000
-// tokens with 8 heads: 63 and 34 us here, 79 and 42 in a kernel like q8_attend.hip's with three and four row tiles; 24 and 32 rows:
-// 35 here, 26 and 27 there.)
+// tokens with 8 heads: 60 and 35 us here, 79 and 42 in a kernel like q8_attend.hip's with three and four row tiles; 24 and 32 rows:
+// 35 here, 27 and 29 there.)
 constexpr int64_t kPromptRows = 32;
 
 Q8Plan q8_prompt_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus) {
@@ -657,7 +657,7 @@ Q8Plan q8_prompt_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len,
     p.row_blocks = (int)((R + p.rows - 1) / p.rows);
     const int tiles = std::max(1, (max_len + kTile - 1) / kTile);
     // Two workgroups of 4 waves from 16 tiles a CU on (below, the pieces are so short that joining more of them costs more): 64 rows
-    // of 4 sequences of 4,000 tokens with 8 heads are 8 a CU, and take 27 us by one workgroup a CU, 29 by two.
+    // of 4 sequences of 4,000 tokens with 8 heads are 8 a CU, and take 27 us by one workgroup a CU, 30 by two.
     const double work = (double)B * H * p.row_blocks * (tiles + kItemCost<true>);
     const int per_cu = d == 64 || (bf16 && p.rows == 128 && work >= 16.0 * cus) ? 2 : 1;
     p.grid = (int)std::min<double>((double)per_cu * cus, (double)B * H * p.row_blocks * tiles);
