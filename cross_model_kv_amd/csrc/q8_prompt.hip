@@ -40,15 +40,19 @@ __device__ __forceinline__ void each(F&& f) {
 constexpr int kTile = 64;
 
 // The weights of bf16 calls are fp16, 2^(y - m): 11 bits from 2^-14 to 2^kTop, fewer below, one at 2^-24.  A row may have nearly all
-// of its weight on a few tokens whose values are zero, and is made of the others then, however far below those they lie;
-// so m follows the scores, up and down, and what fp16 does not hold is not lost.  Where 16 tokens' largest weight is not inside
-// 2^kDrop .. 2^kTop, m moves to the middle of the half tile's scores; there, and where a weight is below 2^kThin, what the rounding
-// takes of the weights below 2^-14 is multiplied on its own, 2^38 times as large (11 bits down to 2^-52).  Scores of a few
-// binades' spread, as 1,024 queries on 33,792 tokens have them, bring this about in one of 1,000 halves; looking for it costs the
-// call 3 % (1,145 -> 1,180 us).  With m at the largest score and no more than that, a row that had 0.9999
-// of its weight on one token lost all of its answer.
-constexpr float kTop = 15.f, kDrop = -11.f, kThin = -24.f;
-constexpr float kLift = 11.f;  // (the middle of scores further apart than fp16 reaches: m is put this far below the largest)
+// of its weight on a few tokens whose values are zero, and is made of the others then, however far below those they lie.  So m
+// follows the scores up and down, and what fp16 does not hold is not lost: where the largest weight of 16 adjacent tokens is not
+// inside 2^kDrop .. 2^kTop, or that of 4 is below 2^kThin, rows that do not fit move their m, and where it is not enough, what the
+// rounding takes of the half tile's weights below 2^-14 is multiplied on its own, 2^38 times as large (11 bits down to 2^-52).  So
+// a weight is off by 2^-11 of the largest of 16 adjacent ones at most.  (With m at the largest score and no more than that, a row that had
+// 0.9999 of its weight on one token lost all of its answer.)  Looking for it costs 2 to 4 % of a call (1,024 queries on 33,792
+// tokens 1,128 -> 1,150 us, on another card 1,170 -> 1,215).  Where scores have a deviation of 2 or 3 nats, as there, it is needed
+// in hardly any half; by 4 the call takes a fifth longer, by 6 more than twice as long: a row then reaches further than fp16 does.
+constexpr float kTop = 15.f, kDrop = -14.f, kThin = -24.f;
+// m is put so far below the largest score of a half: by the item's first half and where it moves down; where it moves up (no more than it
+// has to, for the tokens before); and where it moves down and the half's scores reach further than from there to 2^kThin.
+constexpr float kFirst = 2.f, kUp = 13.f, kWide = 11.f;
+constexpr float kCalm = -8.f;  // rows whose largest weight is below this move along when others move: each on its own costs more
 constexpr float kDeep = 60.f;  // m at most this far below where it has been: 2^60 times 2^15 times 2^30 tokens' codes stays finite
 #define STEP() __builtin_amdgcn_sched_barrier(0)
 
@@ -373,11 +377,15 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
                 top = -inf32();
                 bottom = inf32();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float y = fmaf(x[i], cs, bias);
-                    x[i] = i < see ? y : -inf32();
-                    top = fmaxf(top, x[i]);
-                    if (BF16) bottom = fminf(bottom, i < see ? y : inf32());
+                for (int i = 0; i < 16; i += 4) {
+                    float four = -inf32();
+#pragma unroll
+                    for (int k = i; k < i + 4; ++k) {
+                        x[k] = k < see ? fmaf(x[k], cs, bias) : -inf32();
+                        four = fmaxf(four, x[k]);
+                    }
+                    top = fmaxf(top, four);
+                    if (BF16) bottom = fminf(bottom, four > -inf32() ? four : inf32());
                 }
                 if (BF16) top = top > -inf32() ? top : m;  // (a half that is hidden moves nothing)
                 cs = 1.f;
@@ -397,31 +405,40 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
                     }
                 }
             } else if (__any(fabsf(t - (kTop + kDrop) / 2) > (kTop - kDrop) / 2 || fmaf(bottom, cs, off) < kThin)) {
-                t = fmaf(top, cs, bias);
-                float low = fmaf(bottom, cs, bias);
-                t = fmaxf(t, __shfl_xor(t, 32));
-                low = fminf(low, __shfl_xor(low, 32));
-                const float to = t > m + kTop || t < m + kDrop ? fmaxf(fmaxf(0.5f * t + 0.5f * low - (kTop + kThin) / 2, t - kLift), highest - kDeep) : m;
+                const float own_top = fmaf(top, cs, bias), own_low = fmaf(bottom, cs, bias);  // (of the lane's 16 tokens)
+                t = fmaxf(own_top, __shfl_xor(own_top, 32));
+                const float low = fminf(own_low, __shfl_xor(own_low, 32));
+                float to = m;
+                if (t > m + kTop) to = t - (FIRST ? kFirst : kUp);
+                else if (t < m + kCalm || low < m + kThin) to = fminf(m, fmaxf(t - (low - t < kThin - kFirst ? kWide : kFirst), highest - kDeep));
                 highest = fmaxf(highest, to);
                 const float keep = __builtin_amdgcn_exp2f(m - to);
                 m = to;
                 if constexpr (!FIRST) l *= keep;  // (else nothing is summed yet)
-                if (!FIRST || __any(low < m + kThin)) {
-                    float shift = bias - m;
-                    asm volatile("" : "+v"(shift));  // (or the compiler makes the step's weights here, ahead of its products)
-                    const uint8_t* from_v = s_v + (32 * hi + (tile & 1) * (D * VROW) + 64 * mt);
+                const bool thin = __any(own_low < m + kThin || own_top < m + kDrop);
+                if (!FIRST || thin) {
                     f16x8_t rest[2];
+                    if (thin) {
+                        float shift = bias - m;
+                        asm volatile("" : "+v"(shift));  // (or the compiler makes the step's weights here, ahead of its products)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float p = __builtin_amdgcn_exp2f(fmaf(x[i], cs, shift));
-                        rest[i / 8][i % 8] = (_Float16)(p < 0x1p-14f ? (p - (float)(_Float16)p) * 0x1p38f : 0.f);
+                        for (int i = 0; i < 16; ++i) {
+                            const float p = __builtin_amdgcn_exp2f(fmaf(x[i], cs, shift));
+                            rest[i / 8][i % 8] = (_Float16)(p < 0x1p-14f ? (p - (float)(_Float16)p) * 0x1p38f : 0.f);
+                        }
                     }
+                    const uint8_t* from_v = s_v + (32 * hi + (tile & 1) * (D * VROW) + 64 * mt);
                     each<D / 32>([&](auto I) {
-                        const f16x8_t* v = (const f16x8_t*)(from_v + (c + 32 * I) * VROW);
                         f32x16_t sum;
-                        first_product(v[0], rest[0], sum);
-                        STEP();
-                        next_product(v[1], rest[1], sum);
+                        if (thin) {
+                            const f16x8_t* v = (const f16x8_t*)(from_v + (c + 32 * I) * VROW);
+                            first_product(v[0], rest[0], sum);
+                            STEP();
+                            next_product(v[1], rest[1], sum);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+                        }
                         add_product(o[I], FIRST ? 1.f : keep, sum, 0x1p-38f);
                         STEP();
                     });
@@ -438,9 +455,10 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
         top = -inf32();
         bottom = inf32();
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            top = fmaxf(fmaxf(even[i], even[i + 1]), top);
-            if (BF16) bottom = fminf(fminf(even[i], even[i + 1]), bottom);
+        for (int i = 0; i < 16; i += 4) {
+            const float four = fmaxf(fmaxf(even[i], even[i + 1]), fmaxf(even[i + 2], even[i + 3]));
+            top = fmaxf(top, four);
+            bottom = fminf(bottom, four);
         }
         read_scale(t0, 0);
         use_scale();
@@ -454,8 +472,6 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
             Weights<BF16> w[2];
             float sum[2], p[2];
             const float shift = bias - m;
-            top = -inf32();
-            bottom = inf32();
             // Weight x of the lane's 16 tokens; what is made of x - 2 and x - 1 comes with x, when they are there.
             auto weight = [&](auto X) {
                 constexpr int x = X;
@@ -468,12 +484,19 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
                 }
                 if constexpr (x < E) p[x & 1] = __builtin_amdgcn_exp2f(fmaf(s[x], cs, shift));
             };
+            float four[2];
             auto largest = [&](auto X) {
-                top = fmaxf(fmaxf(next[2 * X], next[2 * X + 1]), top);
-                asm volatile("" : "+v"(top));  // (the same)
-                if constexpr (BF16) {
-                    bottom = fminf(fminf(next[2 * X], next[2 * X + 1]), bottom);
-                    asm volatile("" : "+v"(bottom));
+                constexpr int x = X;
+                float& f = four[x / 2 % 2];
+                f = x % 2 == 0 ? fmaxf(next[2 * x], next[2 * x + 1]) : fmaxf(fmaxf(next[2 * x], next[2 * x + 1]), f);
+                asm volatile("" : "+v"(f));  // (the same)
+                if constexpr (x % 4 == 3) {
+                    top = x == 3 ? fmaxf(four[0], four[1]) : fmaxf(fmaxf(four[0], four[1]), top);
+                    asm volatile("" : "+v"(top));
+                    if constexpr (BF16) {
+                        bottom = x == 3 ? fminf(four[0], four[1]) : fminf(fminf(four[0], four[1]), bottom);
+                        asm volatile("" : "+v"(bottom));
+                    }
                 }
             };
             each<NP>([&](auto F) {
