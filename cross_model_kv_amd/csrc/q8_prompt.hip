@@ -45,9 +45,9 @@ constexpr int kTile = 64;
 // inside 2^kDrop .. 2^kTop, or that of 4 is below 2^kThin, rows that do not fit move their m, and where it is not enough, what the
 // rounding takes of the half tile's weights below 2^-14 is multiplied on its own, 2^38 times as large (11 bits down to 2^-52).  So
 // a weight is off by 2^-11 of the largest of 16 adjacent ones at most.  (With m at the largest score and no more than that, a row that had
-// 0.9999 of its weight on one token lost all of its answer.)  Looking for it costs 2 to 4 % of a call (1,024 queries on 33,792
-// tokens 1,128 -> 1,150 us, on another card 1,170 -> 1,215).  Where scores have a deviation of 2 or 3 nats, as there, it is needed
-// in hardly any half; by 4 the call takes a fifth longer, by 6 more than twice as long: a row then reaches further than fp16 does.
+// 0.9999 of its weight on one token lost all of its answer.)  Looking for it costs 1 to 2 % of a call (1,024 queries on 33,792
+// tokens 1,187 -> 1,204 us).  Where scores have a deviation of 2 or 3 nats, as there, it is needed in hardly any half; by 4 the call
+// takes a sixth longer, by 6 more than twice as long: a row then reaches further than fp16 does.
 constexpr float kTop = 15.f, kDrop = -14.f, kThin = -24.f;
 // m is put so far below the largest score of a half: by the item's first half and where it moves down; where it moves up (no more than it
 // has to, for the tokens before); and where it moves down and the half's scores reach further than from there to 2^kThin.
@@ -145,6 +145,29 @@ __device__ __forceinline__ int fresh_lane() {
     int lane;
     asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(lane));
     return lane;
+}
+
+// The larger, and the smaller, of two or three.  Written out they stay where they are written, and the compiler does not put an
+// instruction in front of each that makes its operands quiet.
+__device__ __forceinline__ float max2(float a, float b) {
+    float r;
+    asm volatile("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm volatile("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float min2(float a, float b) {
+    float r;
+    asm volatile("v_min_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm volatile("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
 }
 
 // What the wave's lanes have written to shared memory is there for its other lanes.
@@ -488,15 +511,10 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
             auto largest = [&](auto X) {
                 constexpr int x = X;
                 float& f = four[x / 2 % 2];
-                f = x % 2 == 0 ? fmaxf(next[2 * x], next[2 * x + 1]) : fmaxf(fmaxf(next[2 * x], next[2 * x + 1]), f);
-                asm volatile("" : "+v"(f));  // (the same)
+                f = x % 2 == 0 ? max2(next[2 * x], next[2 * x + 1]) : max3(next[2 * x], next[2 * x + 1], f);
                 if constexpr (x % 4 == 3) {
-                    top = x == 3 ? fmaxf(four[0], four[1]) : fmaxf(fmaxf(four[0], four[1]), top);
-                    asm volatile("" : "+v"(top));
-                    if constexpr (BF16) {
-                        bottom = x == 3 ? fminf(four[0], four[1]) : fminf(fminf(four[0], four[1]), bottom);
-                        asm volatile("" : "+v"(bottom));
-                    }
+                    top = x == 3 ? max2(four[0], four[1]) : max3(four[0], four[1], top);
+                    if constexpr (BF16) bottom = x == 3 ? min2(four[0], four[1]) : min3(four[0], four[1], bottom);
                 }
             };
             each<NP>([&](auto F) {
