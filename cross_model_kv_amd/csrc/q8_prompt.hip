@@ -9,9 +9,9 @@
 // are 16 adjacent tokens, which is what P^T's operand wants of it: nothing crosses lanes, and the 16
 // tokens lie in one page, with one scale.
 //
-// What bounds it: a tile costs a SIMD (64 rows) 2050 cycles of matrix products, 2470 of issuing vector instructions
-// (these among them) and takes 4300 to 4600; the clock meanwhile falls to 1.7 - 1.9 GHz: 1.12 - 1.23 ms by card for 8,192 rows a head,
-// 8 heads and 33,792 tokens (910 - 1000 TFLOP/s, against 1430 - 1550 of large library products here).  Waves of 64 rows, one a SIMD,
+// What bounds it: a tile costs a SIMD (64 rows) 2050 cycles of matrix products, 2350 of issuing vector instructions
+// (these among them) and takes 4140; the clock meanwhile falls to 1.6 - 1.8 GHz: 1.11 - 1.20 ms by card for 8,192 rows a head,
+// 8 heads and 33,792 tokens (930 - 1000 TFLOP/s, against 1430 - 1550 of large library products here).  Waves of 64 rows, one a SIMD,
 // read half as much shared memory but cannot issue fast enough (an instruction every 5 cycles, 580 of them a tile): the same
 // time within 3 %.  Products next to the vector work in the order in which they are written, not the compiler's, took waves
 // of 64 rows from 1470 us to 1220 - 1300.
@@ -178,8 +178,8 @@ __device__ __forceinline__ void wave_memory() {
 }
 
 // Workgroups that a CU holds at once.  bf16 with 128 dims: one of 8 waves, or two of 4, which have shared memory for two tiles of
-// keys each, not three, and so a barrier more a tile.  (One of 4 waves and three tiles: 64 rows of 8 sequences of 8,192 tokens 68 us
-// for 62, of one of 32,768 39.0 for 37.3.)
+// keys each, not three, and so a barrier more a tile.  (One of 4 waves and three tiles: 64 rows of 8 sequences of 8,192 tokens 66 us
+// for 61.5, of one of 32,768 38 for 37.)
 template <bool BF16, int D, int WAVES>
 constexpr int kPerCu = D == 64 || (BF16 && WAVES == 4) ? 2 : 1;
 
@@ -684,7 +684,7 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
 }  // namespace
 
 // More rows of a sequence and KV head than this take this kernel.  (48 rows in fp32 and 64 in bf16 of 16 sequences of up to 3,000
-// tokens with 8 heads: 60 and 35 us here, 79 and 42 in a kernel like q8_attend.hip's with three and four row tiles; 24 and 32 rows:
+// tokens with 8 heads: 61 and 35 us here, 79 and 42 in a kernel like q8_attend.hip's with three and four row tiles; 24 and 32 rows:
 // 35 here, 27 and 29 there.)
 constexpr int64_t kPromptRows = 32;
 

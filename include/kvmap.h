@@ -563,15 +563,16 @@ int kvmap_q8_dropped(kvmap_ctx* ctx, uint32_t* n, void* stream);
  * A sequence whose len is out of range (negative, above max_len or max_pages * page) gives NaN, and so does a
  * row that sees a token of a page outside 0 .. n_pages - 1.
  * bf16: products with bf16 queries on the matrix cores, softmax weights with 16 bits (up to 32 rows n_q H_q / H_kv) or 11 (more
- * rows: off by 2^-11 of themselves, or 2^-14 of the largest of 16 adjacent tokens), so that the output's own rounding is what counts,
- * however small the part of a row's weight is that its answer is made of; products' sums and statistics in fp32, the sum of a
- * row's weights in fp64 (it spans the values' scales).  fp32: queries and weights as three bf16 parts each, so that products keep
+ * rows: off by 2^-11 of the largest of 16 adjacent tokens' at most), so that the output's own rounding is what counts, however
+ * small the part of a row's weight is that its answer is made of; products' sums and statistics in fp32, the sum of a row's
+ * weights in fp64 (it spans the values' scales).  fp32: queries and weights as three bf16 parts each, so that products keep
  * 24 bits.
  * Repeated calls give identical outputs.  (Where a long cache is cut follows the lengths of all sequences, so a sequence's
  * rounding may differ between calls with different company.)  Asynchronous on `stream`.  Long caches are split over workgroups
  * whose results are joined through a scratch buffer that the context owns: of one size for all calls, allocated
  * by kvmap_q8_reserve or by the first call that needs it, and kept until kvmap_destroy.  A call that would have to
- * allocate it while `stream` is being captured is refused (INVALID_ARGUMENT).  Errors as kvmap_q8_write. */
+ * allocate it while `stream` is being captured is refused (INVALID_ARGUMENT).  Errors as kvmap_q8_write; SHAPE also for
+ * B * H_kv >= 2^16, n_q * H_q >= 2^28, B * n_q * H_q >= 2^31 and max_len >= 2^30. */
 int kvmap_q8_attend(kvmap_ctx* ctx, const kvmap_q8_cache* cache, int32_t layer, int32_t B, int32_t n_q, int32_t H_q,
                     int32_t dtype, const kvmap_q8_rows* q, const int32_t* pages, int32_t max_pages,
                     const int32_t* len, int32_t max_len, double scale, const kvmap_q8_rows* out, float* lse,
