@@ -44,14 +44,16 @@ constexpr int kTile = 64;
 // follows the scores up and down, and what fp16 does not hold is not lost: where the largest weight of 16 adjacent tokens is not
 // inside 2^kDrop .. 2^kTop, or that of 4 is below 2^kThin, rows that do not fit move their m, and where it is not enough, what the
 // rounding takes of the half tile's weights below 2^-14 is multiplied on its own, 2^38 times as large (11 bits down to 2^-52).  So
-// a weight is off by 2^-11 of the largest of 16 adjacent ones at most.  (With m at the largest score and no more than that, a row that had
-// 0.9999 of its weight on one token lost all of its answer.)  Looking for it costs 1 to 2 % of a call (1,024 queries on 33,792
-// tokens 1,187 -> 1,204 us).  Where scores have a deviation of 2 or 3 nats, as there, it is needed in hardly any half; by 4 the call
-// takes a sixth longer, by 6 more than twice as long: a row then reaches further than fp16 does.
+// a weight is off by 2^-11 of the largest of 16 adjacent ones at most, and by 2^-8 of itself next to the row's own token.  (With m
+// at the largest score and no more than that, a row that had 0.9999 of its weight on one token lost all of its answer.)  Looking for
+// it costs 1 to 2 % of a call (1,024 queries on 33,792 tokens 1,107 -> 1,118 us).  Where scores have a deviation of 2 or 3 nats, as there,
+// it is needed in hardly any half; by 4 the call takes a sixth longer, by 6 more than twice as long: a row then reaches further
+// than fp16 does.
 constexpr float kTop = 15.f, kDrop = -14.f, kThin = -24.f;
 // m is put so far below the largest score of a half: by the item's first half and where it moves down; where it moves up (no more than it
 // has to, for the tokens before); and where it moves down and the half's scores reach further than from there to 2^kThin.
-constexpr float kFirst = 2.f, kUp = 13.f, kWide = 11.f;
+constexpr float kFirst = 5.f, kUp = 13.f, kWide = 11.f;
+constexpr float kEdge = -17.f;  // 8 bits: where a row does not see all of a half, which may be few tokens, of every weight that it sees
 constexpr float kCalm = -8.f;  // rows whose largest weight is below this move along when others move: each on its own costs more
 constexpr float kDeep = 60.f;  // m at most this far below where it has been: 2^60 times 2^15 times 2^30 tokens' codes stays finite
 #define STEP() __builtin_amdgcn_sched_barrier(0)
@@ -400,17 +402,16 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
                 top = -inf32();
                 bottom = inf32();
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    float four = -inf32();
-#pragma unroll
-                    for (int k = i; k < i + 4; ++k) {
-                        x[k] = k < see ? fmaf(x[k], cs, bias) : -inf32();
-                        four = fmaxf(four, x[k]);
-                    }
-                    top = fmaxf(top, four);
-                    if (BF16) bottom = fminf(bottom, four > -inf32() ? four : inf32());
+                for (int i = 0; i < 16; ++i) {
+                    const float y = fmaf(x[i], cs, bias);
+                    x[i] = i < see ? y : -inf32();
+                    top = fmaxf(top, x[i]);
+                    if (BF16) bottom = fminf(bottom, i < see ? y : inf32());
                 }
-                if (BF16) top = top > -inf32() ? top : m;  // (a half that is hidden moves nothing)
+                if (BF16) bottom += kThin - kEdge;
+                // 16 hidden tokens move nothing, and a part of 16, often one token or two, only where it keeps fewer than 8 bits (a
+                // repair in one workgroup of a short call is a tenth of it: 16 prompts of 64 tokens 15.6 us, so 14).
+                if (BF16 && (top == -inf32() || top >= m + kEdge)) top = fmaxf(top, m + kCalm);
                 cs = 1.f;
                 bias = 0.f;
             }
@@ -438,7 +439,7 @@ __global__ __launch_bounds__(64 * WAVES, (kPerCu<BF16, D, WAVES> * WAVES / 4)) v
                 const float keep = __builtin_amdgcn_exp2f(m - to);
                 m = to;
                 if constexpr (!FIRST) l *= keep;  // (else nothing is summed yet)
-                const bool thin = __any(own_low < m + kThin || own_top < m + kDrop);
+                const bool thin = __any(own_low < m + kThin || (own_top < m + kDrop && own_low < inf32()));  // (16 hidden tokens are not)
                 if (!FIRST || thin) {
                     f16x8_t rest[2];
                     if (thin) {

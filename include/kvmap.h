@@ -563,9 +563,9 @@ int kvmap_q8_dropped(kvmap_ctx* ctx, uint32_t* n, void* stream);
  * A sequence whose len is out of range (negative, above max_len or max_pages * page) gives NaN, and so does a
  * row that sees a token of a page outside 0 .. n_pages - 1.
  * bf16: products with bf16 queries on the matrix cores, softmax weights with 16 bits (up to 32 rows n_q H_q / H_kv) or 11 (more
- * rows: off by 2^-11 of the largest of 16 adjacent tokens' at most), so that the output's own rounding is what counts, however
- * small the part of a row's weight is that its answer is made of; products' sums and statistics in fp32, the sum of a row's
- * weights in fp64 (it spans the values' scales).  fp32: queries and weights as three bf16 parts each, so that products keep
+ * rows: off by 2^-11 of the largest of 16 adjacent tokens' at most, by 2^-8 of themselves next to the row's own token), so that the
+ * output's own rounding is what counts, however small the part of a row's weight is that its answer is made of; products' sums and
+ * statistics in fp32, the sum of a row's weights in fp64 (it spans the values' scales).  fp32: queries and weights as three bf16 parts each, so that products keep
  * 24 bits.
  * Repeated calls give identical outputs.  (Where a long cache is cut follows the lengths of all sequences, so a sequence's
  * rounding may differ between calls with different company.)  Asynchronous on `stream`.  Long caches are split over workgroups

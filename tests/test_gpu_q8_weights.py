@@ -119,6 +119,19 @@ def test_equal_scores_far_below_the_first_ones(ctx, nats, n_q, G, d, page, dtype
 
 
 @pytest.mark.parametrize("n_q,G,d,page,dtype", SHAPES)
+@pytest.mark.parametrize("before,nats", [(16, 9), (16, 11.5), (16, 12.6), (16, 20), (32, 12.6), (40, 10), (1, 14), (1, 30)])
+def test_a_rows_own_tokens_far_below_the_first_ones(ctx, before, nats, n_q, G, d, page, dtype):
+    """Only the first tokens are seen by all rows, and they have values of zero: a row's answer is made of the queries' own tokens up to
+    it, one for the first row, a part of 16 for most."""
+    T = before + n_q
+    rng = np.random.default_rng([2026, 876, before, int(10 * nats), n_q, G, d, page])
+    levels = np.full(T, -float(nats))
+    levels[:before] = 0
+    o, table, q = _case(rng, T, n_q, 2, G, d, page, dtype, levels, [(slice(None), np.arange(before))])
+    _run(ctx, o, table, q, T, d, dtype, f"own tokens {nats} nats below {before}, n_q {n_q} G {G} d {d} page {page} {dtype}")
+
+
+@pytest.mark.parametrize("n_q,G,d,page,dtype", SHAPES)
 def test_one_page_of_much_larger_values(ctx, n_q, G, d, page, dtype):
     """A page whose values are 2^24 times the others' in one dim and zeros in the rest: its scale is as much larger, which must not cost
     the other pages anything."""
