@@ -10,8 +10,8 @@
 // tokens lie in one page, with one scale.
 //
 // What bounds it: a tile costs a SIMD (64 rows) 2050 cycles of matrix products, 2350 of issuing vector instructions
-// (these among them) and takes 4140; the clock meanwhile falls to 1.6 - 1.8 GHz: 1.11 - 1.20 ms by card for 8,192 rows a head,
-// 8 heads and 33,792 tokens (930 - 1000 TFLOP/s, against 1430 - 1550 of large library products here).  Waves of 64 rows, one a SIMD,
+// (these among them) and takes 4140; the clock meanwhile falls to 1.6 - 1.8 GHz: 1.10 - 1.20 ms by card for 8,192 rows a head,
+// 8 heads and 33,792 tokens (930 - 1015 TFLOP/s, against 1430 - 1550 of large library products here).  Waves of 64 rows, one a SIMD,
 // read half as much shared memory but cannot issue fast enough (an instruction every 5 cycles, 580 of them a tile): the same
 // time within 3 %.  Products next to the vector work in the order in which they are written, not the compiler's, took waves
 // of 64 rows from 1470 us to 1220 - 1300.

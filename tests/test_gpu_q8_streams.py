@@ -41,6 +41,3 @@ def test_outputs_belong_to_the_calls_stream(ctx):
     assert not gone & {x.untyped_storage().data_ptr() for x in (out, lse, got_k, got_v)}
     for got, ref in ((out, want), (lse, want_lse), (got_k, want_k), (got_v, want_v)):
         assert torch.equal(got, ref)
-    # and on the current stream they are that memory
-    gone = freed(want)
-    assert ctx.q8_attend(c, q, pages, lens, n).untyped_storage().data_ptr() in gone
