@@ -22,7 +22,7 @@ LIB = os.path.join(LIB_DIR, "libkvmap.so")
 
 HIP_SOURCES = ["api.hip", "rope.hip", "gemm_bf16.hip", "gemm_bf16_small.hip", "gemm_f32.hip", "gram.hip", "gram_x3.hip",
                "ridge_dev.hip", "fit.hip", "q8_api.hip", "q8_pages.hip", "q8_attend.hip",
-               "q8_prompt.hip", "q8_join.hip"]
+               "q8_prompt.hip", "q8_join.hip", "paged_api.hip", "paged_rows.hip", "paged_attend.hip"]
 HOST_SOURCES = ["ridge.cpp"]
 ARCH = "gfx950"
 

@@ -168,7 +168,7 @@ struct kvmap_ctx {
     void* static_scratch = nullptr;  // this device's copy of `scratch` (kvmap_gram_noalloc)
     TimingRec timing[kTimingRing];  // events of the last kTimingRing KVMAP_FLAG_TIMING applies
     int64_t n_timed = 0;
-    Q8State q8;                   // the 8-bit cache calls' (q8_api.hip)
+    Q8State q8;                   // the paged caches' calls' (q8_api.hip, paged_api.hip)
 };
 
 int kvmap::context_device(const kvmap_ctx* c) { return c ? c->device : -1; }
@@ -230,17 +230,18 @@ extern "C" int kvmap_create(kvmap_ctx** out, int device) {
         }
     }
     const int32_t zero = 0;
+    const unsigned int none[2] = {0, 0};
     if (hipMalloc((void**)&c->d_count, sizeof(unsigned int)) != hipSuccess ||
         hipMalloc((void**)&c->d_zero, sizeof(int32_t)) != hipSuccess) {
         kvmap_destroy(c);
         return fail(KVMAP_ERR_OUT_OF_MEMORY, "kvmap_create: hipMalloc failed");
     }
-    if (hipMalloc((void**)&c->q8.dropped, sizeof(unsigned int)) != hipSuccess) {
+    if (hipMalloc((void**)&c->q8.dropped, sizeof none) != hipSuccess) {
         kvmap_destroy(c);
         return fail(KVMAP_ERR_OUT_OF_MEMORY, "kvmap_create: hipMalloc failed");
     }
     if (hipMemcpy(c->d_zero, &zero, sizeof zero, hipMemcpyHostToDevice) != hipSuccess ||
-        hipMemcpy(c->q8.dropped, &zero, sizeof zero, hipMemcpyHostToDevice) != hipSuccess) {
+        hipMemcpy(c->q8.dropped, none, sizeof none, hipMemcpyHostToDevice) != hipSuccess) {
         kvmap_destroy(c);
         return fail(KVMAP_ERR_DEVICE, "kvmap_create: hipMemcpy failed");
     }
@@ -657,6 +658,23 @@ extern "C" int kvmap_recode(kvmap_ctx* c, int32_t rows, int64_t T, int32_t head_
     const ApplyGeom g{1, 1, rows, head_dim, 1, T};
     const Elem e = dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32;
     KVMAP_HIP(launch_derope(e, src, dst, c->d_zero, 1, g, tab, s));
+    return ok();
+}
+
+extern "C" int kvmap_rope_table(kvmap_ctx* c, const kvmap_rope* rope, int64_t n_pos, int32_t head_dim, float* table,
+                                void* stream) {
+    if (!c) return fail(KVMAP_ERR_INVALID_ARGUMENT, "kvmap_rope_table: ctx is NULL");
+    if (n_pos < 1 || n_pos > (int64_t(1) << 26))
+        return fail(KVMAP_ERR_SHAPE, "kvmap_rope_table: n_pos must be in [1, 2^26]");
+    if (head_dim != 64 && head_dim != 128)
+        return fail(KVMAP_ERR_UNSUPPORTED, "kvmap_rope_table: head_dim %d (64 or 128 supported)", (int)head_dim);
+    const int st = validate_rope(rope, "table", n_pos, head_dim);
+    if (st) return st;
+    if (!table) return fail(KVMAP_ERR_INVALID_ARGUMENT, "kvmap_rope_table: NULL device pointer");
+    if ((uintptr_t)table & 15) return fail(KVMAP_ERR_INVALID_ARGUMENT, "kvmap_rope_table: table must be 16-byte aligned");
+    DeviceGuard guard(c->device);
+    if (!guard.okay) return fail(KVMAP_ERR_DEVICE, "kvmap_rope_table: hipSetDevice(%d) failed", c->device);
+    KVMAP_HIP(launch_rope_table((float2*)table, n_pos, head_dim, make_freqs(rope, head_dim), rope->pos0, (hipStream_t)stream));
     return ok();
 }
 

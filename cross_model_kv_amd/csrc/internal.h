@@ -228,14 +228,36 @@ Q8Plan q8_prompt_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len,
 hipError_t launch_q8_prompt(Elem e, const Q8Attend& a, const Q8Pieces& sp, hipStream_t s);
 hipError_t launch_q8_join(Elem e, const Q8Attend& a, const Q8Pieces& sp, hipStream_t s);
 hipError_t launch_q8_attend(Elem e, const Q8Attend& a, const Q8Plan& p, void* scratch, hipStream_t s);
-// What a context keeps for these calls.
+// What a context keeps for the paged caches' calls.
 struct Q8State {
-    unsigned int* dropped = nullptr;  // pages that writes left out
+    unsigned int* dropped = nullptr;  // [2]: pages that 8-bit writes left out, tokens that appends did
     void* scratch = nullptr;          // attention's partial results
     int device = 0;
     int cus = 0;
 };
 Q8State* q8_state(struct ::kvmap_ctx* c);
+// Allocates the scratch where there is none; `stream` is the call's, or NULL outside of one (q8_api.hip).
+int ensure_scratch(Q8State* s, hipStream_t stream, bool in_call, const char* call);
+
+// ---- paged cache in the model's own type (paged_rows.hip, paged_attend.hip) -----------------------------
+// The pools of the layers that a call works on; rows of d elements, [n_pages][H][page][d] a layer.
+struct PagedPools {
+    char *k, *v;
+    int64_t layer;  // bytes of a layer
+    int n_pages, H, page, d;
+};
+// Cosines and sines [n_pos][d / 2]; tab NULL: nothing is rotated.
+struct Rotation {
+    const float2* tab;
+    int64_t n_pos;
+};
+hipError_t launch_paged_append(Elem e, const PagedPools& c, const Q8Seqs& q, int n_layers, int n, const Q8Rows& k,
+                               const Q8Rows& v, const Rotation& rot, unsigned int* dropped, hipStream_t s);
+hipError_t launch_paged_read(Elem e, const PagedPools& c, const Q8Seqs& q, int n_layers, int n, const Q8Rows& k,
+                             const Q8Rows& v, const Rotation& rot, hipStream_t s);
+// a.c: k and v are one layer's pools, its scales are not used; the scratch is the 8-bit cache's, and so is the join of pieces.
+Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int max_len, bool turn, int cus);
+hipError_t launch_paged_attend(Elem e, const Q8Attend& a, const Rotation& rot, const Q8Plan& p, void* scratch, hipStream_t s);
 
 // Error reporting shared by the C-ABI files: sets the calling thread's last-error string.
 int report(int status, const char* fmt, ...);

@@ -3,51 +3,15 @@
 
 #include "../../include/kvmap.h"
 
-#include <algorithm>
 #include <cmath>
-#include <utility>
 
 #include "internal.h"
+#include "paged_checks.h"
 #include "q8_span.h"
 
 using namespace kvmap;
 
 namespace {
-
-#define Q8_HIP(call)                                                                                  \
-    do {                                                                                              \
-        hipError_t e_ = (call);                                                                       \
-        if (e_ != hipSuccess)                                                                         \
-            return report(e_ == hipErrorOutOfMemory ? KVMAP_ERR_OUT_OF_MEMORY : KVMAP_ERR_DEVICE,     \
-                          "%s: %s (%s:%d)", #call, hipGetErrorString(e_), __FILE__, __LINE__);        \
-    } while (0)
-
-// Makes a device current for the duration of a call (and asks nothing more where it is already).
-struct OnDevice {
-    int prev = -1;
-    bool okay = false;
-    explicit OnDevice(int dev) {
-        int cur = -1;
-        if (hipGetDevice(&cur) != hipSuccess) cur = -1;
-        if (cur == dev) {
-            okay = true;
-            return;
-        }
-        okay = hipSetDevice(dev) == hipSuccess;
-        if (okay) prev = cur;
-    }
-    ~OnDevice() {
-        if (prev >= 0) (void)hipSetDevice(prev);
-    }
-};
-
-constexpr int64_t kMaxElems = int64_t(1) << 46;  // keeps every product of sizes below inside 64 bits
-
-struct Range {
-    const char* at;
-    size_t bytes;
-};
-bool meet(const Range& a, const Range& b) { return a.bytes && b.bytes && a.at < b.at + b.bytes && b.at < a.at + a.bytes; }
 
 int check_cache(const kvmap_q8_cache* c) {
     if (!c) return report(KVMAP_ERR_INVALID_ARGUMENT, "q8 cache is NULL");
@@ -84,46 +48,6 @@ int check_disjoint(const kvmap_q8_cache* c) {
     return KVMAP_OK;
 }
 
-// Rows [layers][B][heads][n][d]: the pointer, the strides, and the memory that they cover.  `twin`: the
-// distance in elements to a second such block with the same strides, which must not share rows with it.
-int check_rows(const kvmap_q8_rows* r, const char* which, int layers, int B, int heads, int n, int d, size_t es,
-               bool output, Range* out, int64_t twin = 0) {
-    if (!r) return report(KVMAP_ERR_INVALID_ARGUMENT, "%s is NULL", which);
-    if (!r->base) return report(KVMAP_ERR_INVALID_ARGUMENT, "%s: NULL device pointer", which);
-    if ((uintptr_t)r->base & 15) return report(KVMAP_ERR_INVALID_ARGUMENT, "%s: the base must be 16-byte aligned", which);
-    std::pair<int64_t, int64_t> dim[5] = {{r->layer_stride, layers}, {r->seq_stride, B}, {r->head_stride, heads},
-                                          {r->token_stride, n}, {twin, twin ? 2 : 1}};
-    std::sort(dim, dim + 5);
-    int64_t reach = d;  // elements from the first to the last of what is covered so far
-    for (auto& [stride, size] : dim) {
-        if (size == 1) continue;  // never stepped
-        if (stride < 0 || stride > kMaxElems || (stride * (int64_t)es) % 16)
-            return report(KVMAP_ERR_INVALID_ARGUMENT, "%s: strides must be >= 0 and whole 16 bytes", which);
-        if (output && stride < reach) return report(KVMAP_ERR_INVALID_ARGUMENT, "%s: output rows overlap", which);
-        if ((double)stride * (double)(size - 1) > (double)kMaxElems) return report(KVMAP_ERR_SHAPE, "%s: too large", which);
-        reach += stride * (size - 1);
-    }
-    *out = {(const char*)r->base, (size_t)reach * es};
-    return KVMAP_OK;
-}
-
-int elem_size(int32_t dtype, size_t* es) {
-    if (dtype != KVMAP_DTYPE_BF16 && dtype != KVMAP_DTYPE_F32) return report(KVMAP_ERR_UNSUPPORTED, "dtype %d unknown", (int)dtype);
-    *es = dtype == KVMAP_DTYPE_BF16 ? 2 : 4;
-    return KVMAP_OK;
-}
-
-int check_table(const kvmap_q8_cache* c, int32_t B, int32_t max_pages, const int32_t* pages) {
-    if (B < 1) return report(KVMAP_ERR_SHAPE, "B must be >= 1");
-    if (max_pages < 1 || (int64_t)max_pages * c->page >= (int64_t(1) << 31))
-        return report(KVMAP_ERR_SHAPE, "max_pages must be >= 1, and max_pages * page below 2^31");
-    if (!pages) return report(KVMAP_ERR_INVALID_ARGUMENT, "pages is NULL");
-    if ((uintptr_t)pages & 3) return report(KVMAP_ERR_INVALID_ARGUMENT, "pages must be 4-byte aligned");
-    return KVMAP_OK;
-}
-
-Range ints(const int32_t* p, int64_t n) { return {(const char*)p, p ? (size_t)n * sizeof(int32_t) : 0}; }
-
 Q8Pools pools(const kvmap_q8_cache* c, int32_t layer0) {
     Q8Pools p;
     p.layer_scales = (int64_t)c->n_pages * c->H_kv;
@@ -139,7 +63,6 @@ Q8Pools pools(const kvmap_q8_cache* c, int32_t layer0) {
     return p;
 }
 
-Q8Rows rows(const kvmap_q8_rows* r) { return {r->base, r->layer_stride, r->seq_stride, r->head_stride, r->token_stride}; }
 
 }  // namespace
 
@@ -154,7 +77,7 @@ extern "C" int kvmap_validate_q8_rows(const kvmap_q8_cache* c, int32_t layer0, i
     if (layer0 < 0 || n_layers < 1 || layer0 > c->L - n_layers)
         return report(KVMAP_ERR_SHAPE, "layers %d .. %d + %d outside [0, %d)", (int)layer0, (int)layer0, (int)n_layers, (int)c->L);
     if (!q) return report(KVMAP_ERR_INVALID_ARGUMENT, "seqs is NULL");
-    st = check_table(c, q->B, q->max_pages, q->pages);
+    st = check_table(c->page, q->B, q->max_pages, q->pages);
     if (st) return st;
     if (!q->start) return report(KVMAP_ERR_INVALID_ARGUMENT, "start is NULL");
     if (((uintptr_t)q->start | (uintptr_t)q->count) & 3)
@@ -180,15 +103,8 @@ extern "C" int kvmap_validate_q8_rows(const kvmap_q8_cache* c, int32_t layer0, i
             if ((output ? j >= 4 : true) && meet(x, r[j]))
                 return report(KVMAP_ERR_INVALID_ARGUMENT, "pages, start or count overlaps what is written");
     if (output && meet(r[4], r[5])) {
-        // keys and values may be parts of one buffer (equal strides), as long as no rows are shared
-        const bool alike = k->layer_stride == v->layer_stride && k->seq_stride == v->seq_stride &&
-                           k->head_stride == v->head_stride && k->token_stride == v->token_stride && k->base != v->base;
-        const bool k_first = (const char*)k->base < (const char*)v->base;
-        const int64_t apart = k_first ? (const char*)v->base - (const char*)k->base : (const char*)k->base - (const char*)v->base;
-        Range both;
-        if (!alike || check_rows(k_first ? k : v, "k and v", n_layers, q->B, c->H_kv, n, c->head_dim, es, true, &both,
-                                 apart / (int64_t)es))
-            return report(KVMAP_ERR_INVALID_ARGUMENT, "k and v overlap");
+        st = check_apart(k, v, n_layers, q->B, c->H_kv, n, c->head_dim, es);
+        if (st) return st;
     }
     report(KVMAP_OK, "%s", "");
     return KVMAP_OK;
@@ -203,7 +119,7 @@ extern "C" int kvmap_q8_write(kvmap_ctx* ctx, const kvmap_q8_cache* c, int32_t l
     Q8State* s = q8_state(ctx);
     OnDevice on(s->device);
     if (!on.okay) return report(KVMAP_ERR_DEVICE, "kvmap_q8_write: hipSetDevice(%d) failed", s->device);
-    Q8_HIP(launch_q8_write(dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32, pools(c, layer0),
+    KVMAP_HIP(launch_q8_write(dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32, pools(c, layer0),
                            {q->pages, q->start, q->count, q->B, q->max_pages}, n_layers, n, rows(k), rows(v), s->dropped,
                            (hipStream_t)stream));
     return KVMAP_OK;
@@ -218,7 +134,7 @@ extern "C" int kvmap_q8_read(kvmap_ctx* ctx, const kvmap_q8_cache* c, int32_t la
     Q8State* s = q8_state(ctx);
     OnDevice on(s->device);
     if (!on.okay) return report(KVMAP_ERR_DEVICE, "kvmap_q8_read: hipSetDevice(%d) failed", s->device);
-    Q8_HIP(launch_q8_read(dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32, pools(c, layer0),
+    KVMAP_HIP(launch_q8_read(dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32, pools(c, layer0),
                           {q->pages, q->start, q->count, q->B, q->max_pages}, n_layers, n, rows(k), rows(v),
                           (hipStream_t)stream));
     return KVMAP_OK;
@@ -230,9 +146,9 @@ extern "C" int kvmap_q8_dropped(kvmap_ctx* ctx, uint32_t* n, void* stream) {
     OnDevice on(s->device);
     if (!on.okay) return report(KVMAP_ERR_DEVICE, "kvmap_q8_dropped: hipSetDevice(%d) failed", s->device);
     unsigned int h = 0;
-    Q8_HIP(hipMemcpyAsync(&h, s->dropped, sizeof h, hipMemcpyDeviceToHost, (hipStream_t)stream));
-    Q8_HIP(launch_fill_zero((float*)s->dropped, 1, (hipStream_t)stream));
-    Q8_HIP(hipStreamSynchronize((hipStream_t)stream));
+    KVMAP_HIP(hipMemcpyAsync(&h, s->dropped, sizeof h, hipMemcpyDeviceToHost, (hipStream_t)stream));
+    KVMAP_HIP(launch_fill_zero((float*)s->dropped, 1, (hipStream_t)stream));
+    KVMAP_HIP(hipStreamSynchronize((hipStream_t)stream));
     *n = h;
     return KVMAP_OK;
 }
@@ -258,7 +174,7 @@ extern "C" int kvmap_validate_q8_attend(const kvmap_q8_cache* c, int32_t layer, 
     st = elem_size(dtype, &es);
     if (st) return st;
     if (layer < 0 || layer >= c->L) return report(KVMAP_ERR_SHAPE, "layer %d outside [0, %d)", (int)layer, (int)c->L);
-    st = check_table(c, B, max_pages, pages);
+    st = check_table(c->page, B, max_pages, pages);
     if (st) return st;
     if (max_len > max_pages * c->page)
         return report(KVMAP_ERR_SHAPE, "max_len %d exceeds max_pages * page = %d", (int)max_len, (int)(max_pages * c->page));
@@ -289,16 +205,16 @@ extern "C" int kvmap_validate_q8_attend(const kvmap_q8_cache* c, int32_t layer, 
 
 // Attention's scratch, of one size for every call: allocated once, so its address never changes under a
 // captured graph.
-static int ensure_scratch(Q8State* s, hipStream_t stream, bool in_call) {
+int kvmap::ensure_scratch(Q8State* s, hipStream_t stream, bool in_call, const char* call) {
     if (s->scratch) return KVMAP_OK;
     if (in_call) {
         hipStreamCaptureStatus capturing = hipStreamCaptureStatusNone;
-        Q8_HIP(hipStreamIsCapturing(stream, &capturing));
+        KVMAP_HIP(hipStreamIsCapturing(stream, &capturing));
         if (capturing != hipStreamCaptureStatusNone)
-            return report(KVMAP_ERR_INVALID_ARGUMENT, "kvmap_q8_attend: the stream is being captured and the context has no scratch "
-                          "yet; call kvmap_q8_reserve first");
+            return report(KVMAP_ERR_INVALID_ARGUMENT, "%s_attend: the stream is being captured and the context has no scratch "
+                          "yet; call %s_reserve first", call, call);
     }
-    Q8_HIP(hipMalloc(&s->scratch, q8_scratch_bytes(s->cus)));
+    KVMAP_HIP(hipMalloc(&s->scratch, q8_scratch_bytes(s->cus)));
     return KVMAP_OK;
 }
 
@@ -310,7 +226,7 @@ extern "C" int kvmap_q8_reserve(kvmap_ctx* ctx, const kvmap_q8_cache* c, int32_t
     Q8State* s = q8_state(ctx);
     OnDevice on(s->device);
     if (!on.okay) return report(KVMAP_ERR_DEVICE, "kvmap_q8_reserve: hipSetDevice(%d) failed", s->device);
-    const int r = ensure_scratch(s, nullptr, false);
+    const int r = ensure_scratch(s, nullptr, false, "kvmap_q8");
     if (r) return r;
     report(KVMAP_OK, "%s", "");
     return KVMAP_OK;
@@ -330,9 +246,9 @@ extern "C" int kvmap_q8_attend(kvmap_ctx* ctx, const kvmap_q8_cache* c, int32_t 
     q8_divisor((uint32_t)(H_q / c->H_kv), a.g_mul, a.g_shift);
     const Q8Plan plan = q8_attend_plan(dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32, B, n_q, H_q, c->H_kv, c->head_dim, max_len, s->cus);
     if (plan.splits) {
-        const int r = ensure_scratch(s, (hipStream_t)stream, true);
+        const int r = ensure_scratch(s, (hipStream_t)stream, true, "kvmap_q8");
         if (r) return r;
     }
-    Q8_HIP(launch_q8_attend(dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32, a, plan, s->scratch, (hipStream_t)stream));
+    KVMAP_HIP(launch_q8_attend(dtype == KVMAP_DTYPE_BF16 ? Elem::BF16 : Elem::F32, a, plan, s->scratch, (hipStream_t)stream));
     return KVMAP_OK;
 }

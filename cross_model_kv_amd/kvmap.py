@@ -99,6 +99,15 @@ class Q8RowsC(ctypes.Structure):
                 ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
 
 
+class PagedCacheC(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class RotationC(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int64)]
+
+
 _lib = None
 
 _SIGS = {
@@ -167,6 +176,23 @@ _SIGS.update({
     "kvmap_q8_attend": (ctypes.c_int, [ctypes.c_void_p] + _Q8_ATTEND + [ctypes.c_void_p]),
     "kvmap_validate_q8_rows": (ctypes.c_int, _Q8_ROWS + [ctypes.c_int32]),
     "kvmap_validate_q8_attend": (ctypes.c_int, _Q8_ATTEND),
+})
+_PAGED_ROWS = [ctypes.POINTER(PagedCacheC), ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(Q8SeqsC), ctypes.c_int32,
+               ctypes.POINTER(Q8RowsC), ctypes.POINTER(Q8RowsC), ctypes.POINTER(RotationC)]
+_PAGED_ATTEND = [ctypes.POINTER(PagedCacheC), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                 ctypes.POINTER(Q8RowsC), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_double,
+                 ctypes.POINTER(RotationC), ctypes.POINTER(Q8RowsC), ctypes.c_void_p]
+_SIGS.update({
+    "kvmap_rope_table": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(Rope), ctypes.c_int64, ctypes.c_int32,
+                                        ctypes.c_void_p, ctypes.c_void_p]),
+    "kvmap_paged_append": (ctypes.c_int, [ctypes.c_void_p] + _PAGED_ROWS + [ctypes.c_void_p]),
+    "kvmap_paged_read": (ctypes.c_int, [ctypes.c_void_p] + _PAGED_ROWS + [ctypes.c_void_p]),
+    "kvmap_paged_dropped": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32), ctypes.c_void_p]),
+    "kvmap_paged_attend": (ctypes.c_int, [ctypes.c_void_p] + _PAGED_ATTEND + [ctypes.c_void_p]),
+    "kvmap_paged_reserve": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(PagedCacheC), ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.c_int32, ctypes.c_int32]),
+    "kvmap_validate_paged_rows": (ctypes.c_int, _PAGED_ROWS + [ctypes.c_int32]),
+    "kvmap_validate_paged_attend": (ctypes.c_int, _PAGED_ATTEND),
 })
 
 
@@ -259,6 +285,23 @@ def validate_q8_attend(cache: Q8CacheC, layer, B, n_q, H_q, dtype, q: Q8RowsC, p
     ref = lambda x: None if x is None else ctypes.byref(x)
     return lib().kvmap_validate_q8_attend(ref(cache), layer, B, n_q, H_q, dtype, ref(q), pages, max_pages, lens,
                                           max_len, scale, ref(out), lse)
+
+
+def validate_paged_rows(cache: PagedCacheC, layer0, n_layers, seqs: Q8SeqsC, n, k: Q8RowsC, v: Q8RowsC, rot: RotationC = None,
+                        output: bool = False) -> int:
+    """kvmap_validate_paged_rows on structs of addresses (nothing is read; None passes NULL); returns the
+    status code (host only, needs no GPU)."""
+    ref = lambda x: None if x is None else ctypes.byref(x)
+    return lib().kvmap_validate_paged_rows(ref(cache), layer0, n_layers, ref(seqs), n, ref(k), ref(v), ref(rot), int(output))
+
+
+def validate_paged_attend(cache: PagedCacheC, layer, B, n_q, H_q, q: Q8RowsC, pages, max_pages, lens, max_len, scale,
+                          out: Q8RowsC, rot: RotationC = None, lse=None) -> int:
+    """kvmap_validate_paged_attend on structs and addresses (nothing is read; None passes NULL); returns the
+    status code (host only, needs no GPU)."""
+    ref = lambda x: None if x is None else ctypes.byref(x)
+    return lib().kvmap_validate_paged_attend(ref(cache), layer, B, n_q, H_q, ref(q), pages, max_pages, lens, max_len, scale,
+                                             ref(rot), ref(out), lse)
 
 
 def ridge_solve_host(mean_x, mean_y, M_xx, M_xy, lam: float, n_threads: int = 0):
@@ -390,6 +433,24 @@ class Q8Cache:
         self.index = k.device.index
 
 
+class PagedCache:
+    """A paged cache in the model's own type (kvmap_paged_cache) over the caller's device tensors:
+    k and v [L][n_pages][H][page][d], bf16 or fp32.  Context.paged_cache allocates one."""
+
+    def __init__(self, k, v):
+        if k.dim() != 5 or v.shape != k.shape:
+            raise ValueError("k and v must be [L][n_pages][H][page][d]")
+        if v.dtype != k.dtype:
+            raise TypeError(f"v dtype {v.dtype} differs from k {k.dtype}")
+        if k.device != v.device:
+            raise ValueError("the cache's tensors must be on one device")
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.L, self.n_pages, self.H, self.page, self.d = (int(x) for x in k.shape)
+        self.c = PagedCacheC(self.L, self.n_pages, self.H, self.page, self.d, _dtype_code(k), _dev_ptr(k, "k"), _dev_ptr(v, "v"))
+        self.ref = ctypes.byref(self.c)
+        self.index = k.device.index
+
+
 class Context:
     """A libkvmap context on one HIP device (kvmap_create / kvmap_destroy)."""
 
@@ -398,9 +459,11 @@ class Context:
         h = ctypes.c_void_p()
         _check(lib().kvmap_create(ctypes.byref(h), self.device), "kvmap_create")
         self._h = h
-        # the 8-bit cache calls' arguments
+        # the paged cache calls' arguments
         self._seqs, self._rows = Q8SeqsC(), (Q8RowsC(), Q8RowsC())
         self._seqs_ref, self._rows_ref = ctypes.byref(self._seqs), tuple(ctypes.byref(r) for r in self._rows)
+        self._rot = RotationC()
+        self._rot_ref = ctypes.byref(self._rot)
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
@@ -518,7 +581,8 @@ class Context:
             raise ValueError(f"{name} must be int32 {list(shape)}")
         return _dev_ptr(t, name)
 
-    def _q8_rows(self, call, cache, k, v, pages, start, n, count, layer, dtype, stream):
+    def _rows_args(self, cache, k, v, pages, start, n, count):
+        """Fills the context's structs with a rows call's arguments; returns the number of layers."""
         B, max_pages = pages.shape
         L = k.shape[0]
         shape = (L, B, cache.H, n, cache.d)
@@ -535,6 +599,10 @@ class Context:
         seqs.B, seqs.max_pages = B, max_pages
         seqs.pages, seqs.start = self._q8_ints(pages, "pages", (B, max_pages)), self._q8_ints(start, "start", (B,))
         seqs.count = None if count is None else self._q8_ints(count, "count", (B,))
+        return L
+
+    def _q8_rows(self, call, cache, k, v, pages, start, n, count, layer, dtype, stream):
+        L = self._rows_args(cache, k, v, pages, start, n, count)
         st = call(self._h, cache.ref, layer, L, self._seqs_ref, n, dtype, self._rows_ref[0], self._rows_ref[1],
                   _stream_of(stream, cache.index))
         if st:
@@ -582,19 +650,13 @@ class Context:
         """kvmap_q8_reserve: allocate the scratch of q8_attend calls of these sizes ahead (before a capture)."""
         _check(lib().kvmap_q8_reserve(self._h, cache.ref, B, n_q, H_q, max_len), "kvmap_q8_reserve")
 
-    def q8_attend(self, cache: Q8Cache, q, pages, lens, max_len: int, layer: int = 0, scale: float | None = None,
-                  out=None, lse=None, stream=None):
-        """kvmap_q8_attend: attention of the last n_q tokens of every sequence, q [B][n_q][H_q][d] (device, bf16 or
-        fp32, any strides of whole 16 bytes over a contiguous head dim), over layer `layer` of the cache.  pages
-        [B][max_pages] and lens [B] are device int32; max_len (host) bounds the lengths; scale defaults to
-        d^-1/2.  Returns out (allocated if not given), or (out, lse) where lse is a float32 [B][n_q][H_q]
-        tensor or True.  What the call allocates belongs to `stream`."""
+    def _attend_args(self, cache, q, out, lse, stream):
+        """Fills the context's rows with q and out, which are allocated, as lse is, where they are not given."""
         torch = _torch()
         shape = q.shape
         if len(shape) != 4 or shape[3] != cache.d:
             raise ValueError(f"q must be [B][n_q][H_q][{cache.d}]")
-        B, n_q, H_q, d = shape
-        max_pages = pages.shape[-1]
+        B, n_q, H_q, _ = shape
         if out is None:
             out = _made_on(stream, lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
         elif out.shape != shape or out.dtype is not q.dtype:
@@ -615,12 +677,126 @@ class Context:
             elif lse.shape != (B, n_q, H_q) or lse.dtype != torch.float32:
                 raise ValueError("lse must be float32 [B][n_q][H_q]")
             lse_ptr = _dev_ptr(lse, "lse")
+        return B, n_q, H_q, out, lse, lse_ptr
+
+    def q8_attend(self, cache: Q8Cache, q, pages, lens, max_len: int, layer: int = 0, scale: float | None = None,
+                  out=None, lse=None, stream=None):
+        """kvmap_q8_attend: attention of the last n_q tokens of every sequence, q [B][n_q][H_q][d] (device, bf16 or
+        fp32, any strides of whole 16 bytes over a contiguous head dim), over layer `layer` of the cache.  pages
+        [B][max_pages] and lens [B] are device int32; max_len (host) bounds the lengths; scale defaults to
+        d^-1/2.  Returns out (allocated if not given), or (out, lse) where lse is a float32 [B][n_q][H_q]
+        tensor or True.  What the call allocates belongs to `stream`."""
+        B, n_q, H_q, out, lse, lse_ptr = self._attend_args(cache, q, out, lse, stream)
+        max_pages = pages.shape[-1]
         st = lib().kvmap_q8_attend(self._h, cache.ref, layer, B, n_q, H_q, _dtype_code(q), self._rows_ref[0],
                                    self._q8_ints(pages, "pages", (B, max_pages)), max_pages,
-                                   self._q8_ints(lens, "lens", (B,)), max_len, d ** -0.5 if scale is None else scale,
+                                   self._q8_ints(lens, "lens", (B,)), max_len, cache.d ** -0.5 if scale is None else scale,
                                    self._rows_ref[1], lse_ptr, _stream_of(stream, cache.index))
         if st:
             _check(st, "kvmap_q8_attend")
+        return out if lse_ptr is None else (out, lse)
+
+    # ---- paged cache in the model's own type -----------------------------------------------
+    def rope_table(self, n_pos: int, d: int, theta: float | None = None, pos0: int = 0, style: int = ROPE_HALF_SPLIT,
+                   inv_freq=None, out=None, stream=None):
+        """kvmap_rope_table: the rotations of positions pos0 .. pos0 + n_pos, float32 [n_pos][d / 2][2] (cosines and sines of
+        theta's or inv_freq's angles), as the paged calls take them."""
+        torch = _torch()
+        if out is None:
+            out = _made_on(stream, lambda: torch.empty((n_pos, d // 2, 2), dtype=torch.float32,
+                                                       device=torch.device("cuda", self.device)))
+        elif out.shape != (n_pos, d // 2, 2) or out.dtype != torch.float32:
+            raise ValueError(f"out must be float32 [{n_pos}][{d // 2}][2]")
+        keep = []
+        rope = _rope(theta, pos0, style, inv_freq, keep)
+        _check(lib().kvmap_rope_table(self._h, ctypes.byref(rope), n_pos, d, _dev_ptr(out, "out"),
+                                      _stream_handle(stream, out.device)), "kvmap_rope_table")
+        return out
+
+    def paged_cache(self, L: int, n_pages: int, H: int, page: int, d: int, dtype=None) -> PagedCache:
+        """An empty PagedCache on the context's device, bf16 unless another dtype is given."""
+        torch = _torch()
+        make = lambda: torch.zeros((L, n_pages, H, page, d), dtype=torch.bfloat16 if dtype is None else dtype,
+                                   device=torch.device("cuda", self.device))
+        return PagedCache(make(), make())
+
+    def _rotation(self, rope, cache):
+        if rope is None:
+            return None
+        shape = rope.shape
+        if len(shape) != 3 or shape[1] != cache.d // 2 or shape[2] != 2 or rope.dtype is not _torch_module.float32:
+            raise ValueError(f"rope must be float32 [positions][{cache.d // 2}][2]")
+        self._rot.table, self._rot.n_pos = _dev_ptr(rope, "rope"), shape[0]
+        return self._rot_ref
+
+    def _paged_rows(self, call, cache, k, v, pages, start, n, count, layer, rope, stream):
+        if k.dtype is not cache.dtype or v.dtype is not cache.dtype:
+            raise TypeError(f"k and v must be of the cache's dtype, {cache.dtype}")
+        if not self.device == cache.index == k.get_device() == v.get_device():
+            raise ValueError("the cache, k and v must be on the context's device")
+        L = self._rows_args(cache, k, v, pages, start, n, count)
+        st = call(self._h, cache.ref, layer, L, self._seqs_ref, n, self._rows_ref[0], self._rows_ref[1],
+                  self._rotation(rope, cache), _stream_of(stream, cache.index))
+        if st:
+            _check(st, call.__name__)
+
+    def paged_append(self, cache: PagedCache, k, v, pages, start, count=None, layer: int = 0, rope=None, stream=None):
+        """kvmap_paged_append: rows k, v [layers][B][H][n][d] (or [B][H][n][d] of one layer; device, the cache's dtype, any
+        strides of whole 16 bytes over a contiguous head dim) enter layers layer .. of the cache as tokens
+        start[b] .. start[b] + count[b] (n each without count) of the sequences whose pages are listed in pages
+        [B][max_pages], the keys rotated at their positions where a table (rope_table) is given.  pages, start and
+        count: device int32."""
+        _torch()
+        if k.dim() == 4:
+            k, v = k.unsqueeze(0), v.unsqueeze(0)
+        if k.dim() != 5:
+            raise ValueError("k and v must be [layers][B][H][n][d] or [B][H][n][d]")
+        self._paged_rows(lib().kvmap_paged_append, cache, k, v, pages, start, k.shape[3], count, layer, rope, stream)
+
+    def paged_read(self, cache: PagedCache, pages, start, n: int, count=None, layer: int = 0, n_layers: int | None = None,
+                   rope=None, out_k=None, out_v=None, stream=None):
+        """kvmap_paged_read: (k, v) [n_layers][B][H][n][d], the n tokens from start[b] of every sequence, zeros past count[b];
+        with a table (rope_table) the keys stripped of their rotation.  n_layers defaults to the layers from `layer`
+        on.  What the call allocates belongs to `stream`."""
+        torch = _torch()
+        L = cache.L - layer if n_layers is None else n_layers
+        if out_k is None:
+            out_k = _made_on(stream, lambda: torch.empty((L, pages.shape[0], cache.H, n, cache.d), dtype=cache.dtype,
+                                                         device=cache.k.device))
+        if out_v is None:
+            out_v = _made_on(stream, lambda: torch.empty_like(out_k, memory_format=torch.contiguous_format))
+        self._paged_rows(lib().kvmap_paged_read, cache, out_k, out_v, pages, start, n, count, layer, rope, stream)
+        return out_k, out_v
+
+    def paged_dropped(self, stream=None) -> int:
+        """kvmap_paged_dropped: tokens that appends left out since the last call (synchronises)."""
+        n = ctypes.c_uint32()
+        _check(lib().kvmap_paged_dropped(self._h, ctypes.byref(n), _stream_handle(stream, self.device)), "kvmap_paged_dropped")
+        return int(n.value)
+
+    def paged_reserve(self, cache: PagedCache, B: int, n_q: int, H_q: int, max_len: int):
+        """kvmap_paged_reserve: allocate the scratch of paged_attend calls of these sizes ahead (before a capture)."""
+        _check(lib().kvmap_paged_reserve(self._h, cache.ref, B, n_q, H_q, max_len), "kvmap_paged_reserve")
+
+    def paged_attend(self, cache: PagedCache, q, pages, lens, max_len: int, layer: int = 0, scale: float | None = None,
+                     rope=None, out=None, lse=None, stream=None):
+        """kvmap_paged_attend: attention of the last n_q (1 to 16) tokens of every sequence, q [B][n_q][H_q][d] (device, the
+        cache's dtype, any strides of whole 16 bytes over a contiguous head dim), over layer `layer` of the cache; with
+        a table (rope_table) the queries are rotated at their positions.  pages [B][max_pages] and lens [B] are device
+        int32; max_len (host) bounds the lengths; scale defaults to d^-1/2.  Returns out (allocated if not given), or
+        (out, lse) where lse is a float32 [B][n_q][H_q] tensor or True.  What the call allocates belongs to `stream`."""
+        if q.dtype is not cache.dtype:
+            raise TypeError(f"q must be of the cache's dtype, {cache.dtype}")
+        if not self.device == cache.index == q.get_device():
+            raise ValueError("the cache and q must be on the context's device")
+        B, n_q, H_q, out, lse, lse_ptr = self._attend_args(cache, q, out, lse, stream)
+        max_pages = pages.shape[-1]
+        st = lib().kvmap_paged_attend(self._h, cache.ref, layer, B, n_q, H_q, self._rows_ref[0],
+                                      self._q8_ints(pages, "pages", (B, max_pages)), max_pages,
+                                      self._q8_ints(lens, "lens", (B,)), max_len, cache.d ** -0.5 if scale is None else scale,
+                                      self._rotation(rope, cache), self._rows_ref[1], lse_ptr, _stream_of(stream, cache.index))
+        if st:
+            _check(st, "kvmap_paged_attend")
         return out if lse_ptr is None else (out, lse)
 
     # ---- fit-side statistics ---------------------------------------------------------

@@ -590,6 +590,87 @@ int kvmap_validate_q8_attend(const kvmap_q8_cache* cache, int32_t layer, int32_t
                              const int32_t* len, int32_t max_len, double scale, const kvmap_q8_rows* out,
                              const float* lse);
 
+/* ---- paged cache in the model's own type ------------------------------------------------------------
+ *
+ * The same pages and tables as the 8-bit cache's, with rows of head_dim elements as the model holds them:
+ * token t of sequence b, head h, lies in row t % page of page pages[b][t / page], keys and values alike.  Its
+ * calls rotate on the way: keys come as a projection leaves them and enter the cache rotated at their positions,
+ * queries are rotated where they are read, and keys read back for the mapping are stripped. */
+typedef struct {
+    int32_t L, n_pages, H_kv, page, head_dim; /* page 16, 32, 64 or 128; head_dim 64 or 128 */
+    int32_t dtype;                            /* kvmap_dtype of the cache and of every row and query in its calls */
+    void* k;                                  /* device [L][n_pages][H_kv][page][head_dim], 16-byte aligned */
+    void* v;                                  /* the same */
+} kvmap_paged_cache;
+
+/* The rotations of positions 0 .. n_pos - 1: cosine and sine of every pair's angle. */
+typedef struct {
+    const float* table; /* device [n_pos][head_dim / 2][2], 16-byte aligned; kvmap_rope_table fills one */
+    int64_t n_pos;      /* 1 .. 2^31 */
+} kvmap_rotation;
+
+/* table[p][i] = (cos a, sin a), a = (rope->pos0 + p) f_i with the frequencies of `rope`, formed in float64.  A caller that
+ * scales its rotations, or whose positions do not run evenly, fills a table of its own.  Asynchronous on `stream`, allocates
+ * nothing.  Errors: SHAPE (n_pos outside 1 .. 2^26), UNSUPPORTED (head_dim, style), INVALID_ARGUMENT. */
+int kvmap_rope_table(kvmap_ctx* ctx, const kvmap_rope* rope, int64_t n_pos, int32_t head_dim, float* table, void* stream);
+
+/* Append tokens start[b] .. start[b] + count[b] of every sequence to layers layer0 .. layer0 + n_layers of the cache.  k, v:
+ * rows (layer - layer0, b, head, i), i < count[b].  With `rot` (NULL: keys enter as they are) pair (x, y) = (i, i + d/2)
+ * of the key at position p enters as (x cos - y sin, y cos + x sin) with row p of the table, formed in fp32 and rounded
+ * once.  Everything else in the pages is left as it is; appending the same tokens again changes nothing.
+ * A token whose position or page is out of range (start < 0, count outside 0 .. n, beyond max_pages, a page outside
+ * 0 .. n_pages - 1, a position not in the table) is not written, and counted: see kvmap_paged_dropped.
+ * Asynchronous on `stream`, allocates nothing, may be captured into a graph.
+ * Errors (nothing written): INVALID_ARGUMENT (NULL, alignment, strides, overlapping buffers), SHAPE (sizes, layer range,
+ * more than 2^27 tokens), UNSUPPORTED (dtype, head_dim, page). */
+int kvmap_paged_append(kvmap_ctx* ctx, const kvmap_paged_cache* cache, int32_t layer0, int32_t n_layers,
+                       const kvmap_q8_seqs* seqs, int32_t n, const kvmap_q8_rows* k, const kvmap_q8_rows* v,
+                       const kvmap_rotation* rot, void* stream);
+/* Read the same tokens: k, v rows (layer - layer0, b, head, i) get them, keys turned by the opposite angles where `rot` is
+ * given (stripped); zeros for count[b] <= i < n, and NaN where an append would have left a token out.  Asynchronous on
+ * `stream`, allocates nothing, may be captured.  Errors as kvmap_paged_append. */
+int kvmap_paged_read(kvmap_ctx* ctx, const kvmap_paged_cache* cache, int32_t layer0, int32_t n_layers,
+                     const kvmap_q8_seqs* seqs, int32_t n, const kvmap_q8_rows* k, const kvmap_q8_rows* v,
+                     const kvmap_rotation* rot, void* stream);
+/* Tokens (whatever their layers and heads; all n of a sequence whose start or count is out of range) that appends on this
+ * context have left out since the last call; *n gets the count, which starts again at 0.  Synchronises `stream`. */
+int kvmap_paged_dropped(kvmap_ctx* ctx, uint32_t* n, void* stream);
+
+/* Attention of the last n_q tokens (1 to 16: a step's own and drafted ones) of every sequence over one layer of the cache:
+ *   y(b, i, h, t) = scale * q(b, i, h) . key(t),  t <= len[b] - n_q + i, key and value head h / (H_q / H_kv)
+ *   lse = log sum_t exp y,   out = sum_t exp(y - lse) value(t)
+ * with q rotated at its position len[b] - n_q + i where `rot` is given (n_pos >= max_len), as kvmap_paged_append rotates
+ * keys; NULL: queries are used as they are.  The queries' own keys and values have been appended before.  A row that sees
+ * no token (len[b] = 0, or row i < n_q - len[b]) gives out = 0 and lse = -infinity.  Tokens that a row does not see do not
+ * touch it, whatever they hold; infinities and NaN in those that it sees reach it as the formula has it (with `rot`, a key
+ * that is not finite makes every row that sees it NaN).
+ * q, out, pages, max_pages, len, max_len, lse, and what is out of range: as in kvmap_q8_attend, with rows of the cache's dtype.
+ * bf16: products on the matrix cores with bf16 operands, softmax weights with 16 bits and queries that were rotated with 24.  fp32:
+ * products of fp32 operands.  Products' sums and statistics in fp32, the sum of a row's weights in fp64.
+ * Repeated calls give identical outputs.  (Where a long cache is cut follows the lengths of all sequences, so a sequence's
+ * rounding may differ between calls with different company.)  Asynchronous on `stream`.  Long caches are split over
+ * workgroups whose results are joined through the context's scratch, as in kvmap_q8_attend and shared with it: calls that may
+ * run at the same time, two graphs' replays among them, need a context each.  A call that would have to allocate it while
+ * `stream` is being captured is refused (INVALID_ARGUMENT): kvmap_paged_reserve.  Errors as kvmap_paged_append; SHAPE also for
+ * B * H_kv >= 2^16, H_q > 2^16, B * n_q * H_q >= 2^24, max_len >= 2^30 and a table shorter than max_len; UNSUPPORTED also for
+ * n_q > 16. */
+int kvmap_paged_attend(kvmap_ctx* ctx, const kvmap_paged_cache* cache, int32_t layer, int32_t B, int32_t n_q, int32_t H_q,
+                       const kvmap_q8_rows* q, const int32_t* pages, int32_t max_pages, const int32_t* len,
+                       int32_t max_len, double scale, const kvmap_rotation* rot, const kvmap_q8_rows* out, float* lse,
+                       void* stream);
+/* Prepare for kvmap_paged_attend calls of this cache, B, n_q, H_q and max_len: allocates the scratch where there is none
+ * yet.  Refused as kvmap_paged_attend refuses the sizes.  Synchronous. */
+int kvmap_paged_reserve(kvmap_ctx* ctx, const kvmap_paged_cache* cache, int32_t B, int32_t n_q, int32_t H_q, int32_t max_len);
+/* Host-only checks of the calls above, run by them before any device work (buffers are taken as addresses, nothing is
+ * read).  `output` != 0: the rows are written (kvmap_paged_read).  Need no device. */
+int kvmap_validate_paged_rows(const kvmap_paged_cache* cache, int32_t layer0, int32_t n_layers, const kvmap_q8_seqs* seqs,
+                              int32_t n, const kvmap_q8_rows* k, const kvmap_q8_rows* v, const kvmap_rotation* rot,
+                              int32_t output);
+int kvmap_validate_paged_attend(const kvmap_paged_cache* cache, int32_t layer, int32_t B, int32_t n_q, int32_t H_q,
+                                const kvmap_q8_rows* q, const int32_t* pages, int32_t max_pages, const int32_t* len,
+                                int32_t max_len, double scale, const kvmap_rotation* rot, const kvmap_q8_rows* out,
+                                const float* lse);
+
 #ifdef __cplusplus
 }
 #endif
