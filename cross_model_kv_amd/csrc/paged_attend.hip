@@ -11,15 +11,15 @@
 //   S^T = K Q^T   16 tokens x 16 rows, twice   -> lane holds 4 tokens of one row
 //   O^T = V^T P^T 16 dims x 16 rows            -> lane holds 4 dims of one row
 // The order of a contraction is free as long as both operands share it, and so are the orders of S^T's tokens and of
-// O^T's dims.  They are chosen so that nothing crosses lanes: with g = lane >> 4, row 4 g' + j of S^T's tile m is token
+// O^T's dims.  They are chosen so that no score crosses lanes: with g = lane >> 4, row 4 g' + j of S^T's tile m is token
 // 8 g' + 4 m + j, so that lane group g ends up with the tokens 8 g .. 8 g + 7 of its row; and row c of O^T's tile
 // (half, j) is dim 64 half + 4 c + j, so that a lane reads 4 adjacent dims of each of those 8 tokens.  For bf16 products
 // (16x16x32) the 8 tokens of a dim are brought side by side by byte permutes; fp32 products (16x16x4) take a token at
-// a time and need none.  No shared memory and no barrier in the loop.
+// a time and need none.  No shared memory and no barrier in the loop but for the low parts of turned queries.
 //
 // bf16 calls: weights as two bf16 parts (16 bits, fp32's exponents: a weight counts however far below the row's largest
-// it lies), queries that were turned as three (24 bits, what their turn in fp32 has).  fp32 calls:
-// products of fp32 operands.  Sums and statistics in fp32, a row's sum of weights in fp64.
+// it lies), queries that were turned as three (24 bits, what their turn in fp32 has).  fp32 calls: products of fp32
+// operands.  Sums and statistics in fp32, a row's sum of weights in fp64.
 
 #include <algorithm>
 #include <type_traits>
@@ -32,54 +32,88 @@
 namespace kvmap {
 namespace {
 
-constexpr int kTile = kPagedStep / kWaves;  // tokens of a wave's step
-static_assert(kTile == 32, "the tiles' token order");
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-// A row's queries as operands of S^T, and a tile's keys: 16 bytes of a token's dims a step.
+constexpr int kTile = 32;  // tokens of a wave's step
+
+// A row's queries as operands of S^T.  load() asks for what ready() makes them of; low: the lane's place in shared memory for
+// the second and third parts of turned bf16 queries (N rows tiles side by side), which all waves share.
 template <bool BF16, int D, bool TURN>
 struct Queries;
+
+// From this many row tiles on, the low parts of turned queries are in shared memory.
+constexpr int kShared = 2;
 
 template <int D, bool TURN>
 struct Queries<true, D, TURN> {
     static constexpr int STEPS = D / 32;  // step s contracts dims 32 s + 8 g .. + 8
-    static constexpr int N = TURN ? 3 : 1;
-    Parts<N> p[STEPS];
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-            for (int k = 0; k < N; ++k) p[s].p[k] = bf16x8_t{};
-    }
+    bf16x8_t p[STEPS];
+    u32x4_t own[2 * STEPS];
+    f32x4_t t[TURN ? STEPS * 2 : 1];
     // row: the query's first element; tab: its position's cosines and sines
     __device__ __forceinline__ void load(const void* row, int g, const float2* tab) {
         const __bf16* at = (const __bf16*)row + 8 * g;
-        if (!TURN) {
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) p[s].p[0] = *(const bf16x8_t*)(at + 32 * s);
-            return;
-        }
+        for (int s = 0; s < STEPS; ++s) p[s] = *(const bf16x8_t*)(at + 32 * s);
+        if (TURN)
+#pragma unroll
+            for (int s = 0; s < STEPS / 2; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[4 * s + e] = *(const f32x4_t*)(tab + 32 * s + 8 * g + 2 * e);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) p[s] = bf16x8_t{};
+        if (TURN)
+#pragma unroll
+            for (int s = 0; s < STEPS * 2; ++s) t[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    template <int N>
+    __device__ __forceinline__ void ready(u32x4_t* low, bool write) {
+        if (!TURN) return;
 #pragma unroll
         for (int s = 0; s < STEPS / 2; ++s) {
-            const bf16x8_t lo = *(const bf16x8_t*)(at + 32 * s), hi = *(const bf16x8_t*)(at + 32 * s + D / 2);
             float a[8], b[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float2 t = tab[32 * s + 8 * g + e];
-                const float x = (float)lo[e], y = (float)hi[e];
-                a[e] = fmaf(-y, t.y, x * t.x);
-                b[e] = fmaf(x, t.y, y * t.x);
+                const float x = (float)p[s][e], y = (float)p[s + STEPS / 2][e];
+                const float cs = t[4 * s + e / 2][2 * (e & 1)], sn = t[4 * s + e / 2][2 * (e & 1) + 1];
+                a[e] = fmaf(-y, sn, x * cs);
+                b[e] = fmaf(x, sn, y * cs);
             }
-            p[s].set(a);
-            p[s + STEPS / 2].set(b);
+            Parts<3> lo, hi;
+            lo.set(a);
+            hi.set(b);
+            p[s] = lo.p[0];
+            p[s + STEPS / 2] = hi.p[0];
+            if (N < kShared)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    own[k * STEPS + s] = __builtin_bit_cast(u32x4_t, lo.p[1 + k]);
+                    own[k * STEPS + s + STEPS / 2] = __builtin_bit_cast(u32x4_t, hi.p[1 + k]);
+                }
+            else if (write)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    low[(k * STEPS + s) * N * 64] = __builtin_bit_cast(u32x4_t, lo.p[1 + k]);
+                    low[(k * STEPS + s + STEPS / 2) * N * 64] = __builtin_bit_cast(u32x4_t, hi.p[1 + k]);
+                }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
-    __device__ __forceinline__ f32x4_t times(const u32x4_t (&k)[STEPS]) const {
-        f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+    // s0, s1 += step st of two tiles of keys
+    template <int N>
+    __device__ __forceinline__ void times(const u32x4_t (&k)[2], int st, const u32x4_t* low, f32x4_t& s0, f32x4_t& s1) const {
+        const bf16x8_t x0 = __builtin_bit_cast(bf16x8_t, k[0]), x1 = __builtin_bit_cast(bf16x8_t, k[1]);
+        if (TURN)
 #pragma unroll
-        for (int st = 0; st < STEPS; ++st)
-#pragma unroll
-            for (int n = N; n--;) s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, k[st]), p[st].p[n], s, 0, 0, 0);
-        return s;
+            for (int part = 1; part >= 0; --part) {
+                const bf16x8_t y = __builtin_bit_cast(bf16x8_t, N < kShared ? own[part * STEPS + st] : low[(part * STEPS + st) * N * 64]);
+                s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x0, y, s0, 0, 0, 0);
+                s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x1, y, s1, 0, 0, 0);
+            }
+        s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x0, p[st], s0, 0, 0, 0);
+        s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x1, p[st], s1, 0, 0, 0);
     }
 };
 
@@ -87,33 +121,99 @@ template <int D, bool TURN>
 struct Queries<false, D, TURN> {
     static constexpr int STEPS = D / 16;  // step s contracts dims 16 s + 4 g .. + 4
     f32x4_t p[STEPS];
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) p[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
+    f32x4_t t[TURN ? STEPS : 1];
     __device__ __forceinline__ void load(const void* row, int g, const float2* tab) {
         const float* at = (const float*)row + 4 * g;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) p[s] = *(const f32x4_t*)(at + 16 * s);
+        if (TURN)
+#pragma unroll
+            for (int s = 0; s < STEPS / 2; ++s)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) t[2 * s + e] = *(const f32x4_t*)(tab + 16 * s + 4 * g + 2 * e);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) p[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if (TURN)
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) t[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    template <int N>
+    __device__ __forceinline__ void ready(u32x4_t*, bool) {
         if (!TURN) return;
 #pragma unroll
         for (int s = 0; s < STEPS / 2; ++s)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 t = tab[16 * s + 4 * g + e];
                 const float x = p[s][e], y = p[s + STEPS / 2][e];
-                p[s][e] = fmaf(-y, t.y, x * t.x);
-                p[s + STEPS / 2][e] = fmaf(x, t.y, y * t.x);
+                const float cs = t[2 * s + e / 2][2 * (e & 1)], sn = t[2 * s + e / 2][2 * (e & 1) + 1];
+                p[s][e] = fmaf(-y, sn, x * cs);
+                p[s + STEPS / 2][e] = fmaf(x, sn, y * cs);
             }
     }
-    __device__ __forceinline__ f32x4_t times(const u32x4_t (&k)[STEPS]) const {
-        f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+    template <int N>
+    __device__ __forceinline__ void times(const u32x4_t (&k)[2], int st, const u32x4_t*, f32x4_t& s0, f32x4_t& s1) const {
 #pragma unroll
-        for (int st = 0; st < STEPS; ++st)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[st][e]), p[st][e], s, 0, 0, 0);
-        return s;
+        for (int e = 0; e < 4; ++e) {
+            s0 = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[0][e]), p[st][e], s0, 0, 0, 0);
+            s1 = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[1][e]), p[st][e], s1, 0, 0, 0);
+        }
     }
+};
+
+template <bool STREAM, class T>
+__device__ __forceinline__ T fetch(const T* p) { return STREAM ? __builtin_nontemporal_load(p) : *p; }
+
+// A tile's keys, as operands of S^T: step st of tile mt is bytes 64 st + 16 g of row c.  at0, at1: where the lane's rows of
+// the tile's first and last 16 tokens are.
+template <bool BF16, int D>
+struct Keys;
+
+// bf16: a load brings whole lines of 128 bytes, of 8 tokens: lane (c, g) gets bytes 64 (c >> 3) + 16 g of the lines of row
+// (c & 7) + 8 j, and lanes 8 apart change halves.
+template <int D>
+struct Keys<true, D> {
+    static constexpr int LINES = D / 64, STEPS = 2 * LINES;
+    u32x4_t k[2][2][LINES];  // [mt][j][line]
+    __device__ static __forceinline__ int token(int c) { return 8 * ((c >> 2) & 1) + (c & 3); }
+    __device__ static __forceinline__ int byte(int c, int g) { return 64 * (c >> 3) + 16 * g; }
+    template <bool STREAM>
+    __device__ __forceinline__ void load(const char* at0, const char* at1) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int l = 0; l < LINES; ++l) k[mt][j][l] = fetch<STREAM>((const u32x4_t*)((j ? at1 : at0) + 4 * mt * D * 2 + 128 * l));
+    }
+    __device__ __forceinline__ u32x4_t step(int mt, int st) const {
+        const u32x4_t a = k[mt][0][st >> 1], b = k[mt][1][st >> 1];
+        u32x4_t x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = st & 1 ? (uint32_t)__builtin_amdgcn_update_dpp((int)b[i], (int)a[i], 0x128, 0xF, 0x3, false)
+                          : (uint32_t)__builtin_amdgcn_update_dpp((int)a[i], (int)b[i], 0x128, 0xF, 0xC, false);
+        return x;
+    }
+};
+
+// fp32: half a line of 16 tokens a load, as the product wants them.
+template <int D>
+struct Keys<false, D> {
+    static constexpr int STEPS = D / 16;
+    u32x4_t k[2][STEPS];
+    __device__ static __forceinline__ int token(int c) { return 8 * ((c >> 2) & 1) + (c & 3); }
+    __device__ static __forceinline__ int byte(int, int g) { return 16 * g; }
+    template <bool STREAM>
+    __device__ __forceinline__ void load(const char* at0, const char* at1) {
+        const char* at = threadIdx.x & 8 ? at1 : at0;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) k[mt][s] = *(const u32x4_t*)(at + 4 * mt * D * 4 + 64 * s);
+    }
+    __device__ __forceinline__ u32x4_t step(int mt, int st) const { return k[mt][st]; }
 };
 
 // The weights of a lane's 8 tokens.  In bf16 as two parts, the first cut off, so that the second is not negative, and not
@@ -158,35 +258,34 @@ struct Values;
 template <int D>
 struct Values<true, D> {
     typedef RowWeights<true> Weights;
-    uint2 v[8][D / 64];
+    u32x2_t v[8][D / 64];
+    template <bool STREAM>
     __device__ __forceinline__ void load(const char* at, int row) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) v[e][h] = *(const uint2*)(at + e * row + 128 * h);
+            for (int h = 0; h < D / 64; ++h) v[e][h] = fetch<STREAM>((const u32x2_t*)(at + e * row + 128 * h));
     }
     __device__ __forceinline__ void keep(int e, bool yes) {
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-            v[e][h].x = yes ? v[e][h].x : 0u;
-            v[e][h].y = yes ? v[e][h].y : 0u;
-        }
+        for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) v[e][h][i] = yes ? v[e][h][i] : 0u;
     }
     __device__ __forceinline__ bool finite(int e) const {
         bool ok = true;
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
-            for (uint32_t w : {v[e][h].x, v[e][h].y}) ok &= (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ok &= (v[e][h][i] & 0x7F80u) != 0x7F80u && (v[e][h][i] & 0x7F800000u) != 0x7F800000u;
         return ok;
     }
     // dim 64 half + 4 c + j of the 8 tokens
     __device__ __forceinline__ bf16x8_t dim(int half, int j) const {
         u32x4_t w;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t a = j & 2 ? v[2 * e][half].y : v[2 * e][half].x, b = j & 2 ? v[2 * e + 1][half].y : v[2 * e + 1][half].x;
-            w[e] = __builtin_amdgcn_perm(b, a, j & 1 ? 0x07060302u : 0x05040100u);
-        }
+        for (int e = 0; e < 4; ++e)
+            w[e] = __builtin_amdgcn_perm(v[2 * e + 1][half][j >> 1], v[2 * e][half][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
         return __builtin_bit_cast(bf16x8_t, w);
     }
     __device__ __forceinline__ f32x4_t times(int half, int j, const Weights& w, f32x4_t o) const { return w.times(dim(half, j), o); }
@@ -203,11 +302,12 @@ template <int D>
 struct Values<false, D> {
     typedef RowWeights<false> Weights;
     f32x4_t v[8][D / 64];
+    template <bool STREAM>
     __device__ __forceinline__ void load(const char* at, int row) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) v[e][h] = *(const f32x4_t*)(at + e * row + 256 * h);
+            for (int h = 0; h < D / 64; ++h) v[e][h] = fetch<STREAM>((const f32x4_t*)(at + e * row + 256 * h));
     }
     __device__ __forceinline__ void keep(int e, bool yes) {
 #pragma unroll
@@ -235,44 +335,90 @@ struct Values<false, D> {
     }
 };
 
-// Workgroups that a CU holds at once, as the registers and the shared memory allow.
-__host__ __device__ constexpr int per_cu(bool bf16, int nt, bool turn) { return bf16 ? (nt == 1 ? (turn ? 2 : 3) : (turn ? 1 : 2)) : (nt == 1 ? 2 : 1); }
-
-// Steps of one item of each of 64 sequences, summed up to and including the lane's.
-__device__ __forceinline__ uint32_t steps_upto(const Q8Attend& a, int b0, int lane) {
-    return wave_scan(b0 + lane < a.B ? (uint32_t)paged_steps(a.len[b0 + lane], a.max_len) : 0u);
+// Whether one of the tokens from .. to of a lane's 8 has values that are not finite.
+template <class V>
+__device__ __forceinline__ bool odd(const V& v, int from, int to) {
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) any |= e >= from && e < to && !v.finite(e);
+    return any;
 }
 
-template <bool BF16, int D, int NT, bool TURN>
-__global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_kernel(Q8Attend a, Rotation rot, Q8Pieces sp) {
-    constexpr int ROWS = 16 * NT, ES = BF16 ? 2 : 4, LDO = D + 4;
+// Waves that a SIMD holds at once, as the registers allow.
+__host__ __device__ constexpr int per_simd(bool bf16, int d, int nt, bool turn) {
+    if (d == 64) return nt == 2 ? 2 : bf16 ? 4 : 3;
+    return nt == 2 ? (bf16 ? 2 : 1) : bf16 && !turn ? 3 : 2;
+}
+// Waves of a workgroup.
+__host__ __device__ constexpr int waves_of(bool bf16, int d, int nt, bool turn) { return nt == 2 && per_simd(bf16, d, nt, turn) > 1 ? 8 : 4; }
+
+// Steps of one item of each of 64 sequences, summed up to and including the lane's.
+__device__ __forceinline__ uint32_t steps_upto(const Q8Attend& a, int b0, int step, int lane) {
+    return wave_scan(b0 + lane < a.B ? (uint32_t)steps_of(a.len[b0 + lane], a.max_len, step) : 0u);
+}
+
+// One row and 4 dims of a workgroup's waves' sums, joined.
+template <int W, int ROWS, int LDO>
+__device__ __forceinline__ void join_own(const float (*o)[ROWS][LDO], const float (*ml)[ROWS][2], int row, int d4, float& top,
+                                         float& lsum, f32x4_t& sum) {
+    top = ml[0][row][0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = fmaxf(top, ml[w][row][0]);
+    sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    lsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml[w][row][0] - top);
+        sum += f * *(const f32x4_t*)&o[w][row][d4];
+        lsum = fmaf(f, ml[w][row][1], lsum);
+    }
+}
+
+template <bool BF16, int D, int NT, bool TURN, bool STREAM, int W>
+__global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT, TURN))) void paged_decode_kernel(Q8Attend a, Rotation rot, Q8Pieces sp) {
+    constexpr int ROWS = 16 * NT, ES = BF16 ? 2 : 4, LDO = D + 4, THREADS = 64 * W, STEP = kTile * W;
+    constexpr bool SHARES = BF16 && TURN && NT >= kShared;
+    constexpr int LOW = SHARES ? 2 * (D / 32) * NT * 64 : 1;
     typedef Queries<BF16, D, TURN> Q;
     typedef Values<BF16, D> V;
     typedef RowWeights<BF16> Weights;
-    __shared__ float s_o[kWaves][ROWS][LDO];
-    __shared__ float s_ml[kWaves][ROWS][2];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int c = lane & 15, g = lane >> 4;
+    __shared__ float s_o[W][ROWS][LDO];
+    __shared__ float s_ml[W][ROWS][2];
+    __shared__ u32x4_t s_low[LOW];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int H = a.c.H, G = a.Hq / H, R = a.n_q * G;
     const int P = a.c.page, logP = 31 - __clz(P);
     const int items = H * sp.row_blocks;  // of one sequence
     const float y2 = a.scale * kLog2e;
     const bool cuts = sp.cut != nullptr;
-
+    const int lane0 = threadIdx.x & 63;
     // Where items may be cut: this workgroup's piece [at, stop) of the line of steps, and the sequence that it begins in.
     // Else whole items, one after the other.
-    uint64_t at = blockIdx.x, stop = (uint64_t)a.B * items, share = 1, base = 0;
+    uint64_t stop = (uint64_t)a.B * items, share = 1, base = 0;
+    uint32_t upto = 0, used = gridDim.x;
     int b = 0;
     if (cuts) {
-        uint32_t upto = steps_upto(a, 0, lane);
+        upto = steps_upto(a, 0, STEP, lane0);
         uint64_t total = lane_value(upto, 63);
-        for (int b0 = 64; b0 < a.B; b0 += 64) total += lane_value(steps_upto(a, b0, lane), 63);
-        total *= items;
+        for (int b0 = 64; b0 < a.B; b0 += 64) total += lane_value(steps_upto(a, b0, STEP, lane0), 63);
+        stop = total *= items;
         share = div64(total + gridDim.x - 1, gridDim.x);
-        at = share * blockIdx.x;
-        stop = at + share < total ? at + share : total;
-        if (tid == 255 && !sp.few) sp.cut[blockIdx.x] = make_int2(0, 1);  // (by the thread that may write it again)
-        if (at >= stop) return;
+        if (4 * per_simd(BF16, D, NT, TURN) / W == 3 && gridDim.x % 3 == 0) {
+            const uint64_t two = gridDim.x / 3 * 2, share2 = div64(total + two - 1, two);
+            if (34 * share2 < 48 * share) share = share2;
+        }
+        used = (uint32_t)div64(total + share - 1, share);
+        if (blockIdx.x >= used) {
+            if (threadIdx.x == 0 && !sp.few) sp.cut[blockIdx.x] = make_int2(0, 1);
+            return;
+        }
+    }
+    // neighbouring pieces on one XCD (workgroups go round the 8 XCDs), so that the heads of a page meet in its caches
+    const uint32_t xcd = blockIdx.x % 8, piece = xcd * (used / 8) + min(xcd, used % 8) + blockIdx.x / 8;
+    uint64_t at = share * piece;
+    if (cuts) {
+        stop = min(stop, at + share);
+        if (threadIdx.x == THREADS - 1 && !sp.few) sp.cut[piece] = make_int2(0, 1);  // (by the thread that may write it again)
         for (int b0 = 0;;) {
             const uint64_t past = __ballot(base + (uint64_t)upto * items > at);
             if (past) {
@@ -284,7 +430,7 @@ __global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_ke
             base += (uint64_t)lane_value(upto, 63) * items;
             b0 += 64;
             if (b0 >= a.B) return;  // (not reached while the lengths stay as they were summed)
-            upto = steps_upto(a, b0, lane);
+            upto = steps_upto(a, b0, STEP, lane0);
         }
     }
 
@@ -293,7 +439,7 @@ __global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_ke
         uint64_t item_at = 0;
         if (cuts) {
             b = __builtin_amdgcn_readfirstlane(b);
-            steps = paged_steps(a.len[b], a.max_len);
+            steps = steps_of(a.len[b], a.max_len, STEP);
             const uint64_t next = base + (uint64_t)steps * items;
             if (at >= next) {
                 base = next;
@@ -307,20 +453,23 @@ __global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_ke
         } else {
             b = __builtin_amdgcn_readfirstlane((int)((uint32_t)at / (uint32_t)items));
             item = (int)((uint32_t)at - (uint32_t)b * (uint32_t)items);
-            s_end = steps = paged_steps(a.len[b], a.max_len);
+            s_end = steps = steps_of(a.len[b], a.max_len, STEP);
         }
         item = __builtin_amdgcn_readfirstlane(item);
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));  // keeps products of it with strides from being held across items: registers are full
+        const int lane = tid & 63, c = lane & 15, g = lane >> 4;
         const int len = a.len[b];
         const bool bad = len < 0 || len > a.max_len;
         const int tiles = bad ? 0 : (len + kTile - 1) / kTile;
         const int h = item / sp.row_blocks, rb = item - h * sp.row_blocks;
-        const int t_begin = s_begin * kWaves, t_end = min(tiles, s_end * kWaves);
+        const int t_begin = s_begin * W, t_end = min(tiles, s_end * W);
 
         const int32_t* pages = a.pages + (int64_t)b * a.max_pages;
         // the pages of a tile's first and last 16 tokens
         auto page_of = [&](int tile, int half) { return q8_page_at(pages, (int64_t)(tile * kTile + 16 * half) >> logP, a.max_pages, a.c.n_pages); };
         int tile = t_begin + wave;
-        int p0 = -1, p1 = -1;
+        int p0 = -1, p1 = -1, n0 = -1, n1 = -1;  // of the tile in hand, and of the next one
         if (tile < t_end) p0 = page_of(tile, 0), p1 = page_of(tile, 1);
 
         // this lane's rows: their queries, and the tokens that they see
@@ -341,6 +490,26 @@ __global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_ke
                 q[n].zero();
             }
         }
+        // A tile's keys and values.  A lane's 8 tokens of values lie in one page, which has whole 16 tokens, and so do the rows of
+        // keys of one load.  What one workgroup alone reads is read past the caches (STREAM).
+        Keys<BF16, D> k;
+        V v;
+        const char* kbase = (const char*)a.c.k + Keys<BF16, D>::byte(c, g);
+        auto load_keys = [&](int t0, int p0, int p1) {
+            const int tk = t0 + Keys<BF16, D>::token(c);
+            k.template load<STREAM>(kbase + ((((int64_t)max(p0, 0) * H + h) * P + (tk & (P - 1))) * D) * ES,
+                                    kbase + ((((int64_t)max(p1, 0) * H + h) * P + ((tk + 16) & (P - 1))) * D) * ES);
+        };
+        auto values_at = [&](int t0, int p0, int p1) {
+            const int tv = t0 + 8 * g, pv = g & 2 ? p1 : p0;
+            return (const char*)a.c.v + ((((int64_t)max(pv, 0) * H + h) * P + (tv & (P - 1))) * D + 4 * c) * ES;
+        };
+        if (tile + W < t_end) n0 = page_of(tile + W, 0), n1 = page_of(tile + W, 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) q[n].template ready<NT>(s_low + n * 64 + lane, wave == 0);
+        if (SHARES) __syncthreads();
+        int low = lane;
+
         f32x4_t o[NT][D / 16];
         float m[NT];
         double l[NT];
@@ -351,32 +520,32 @@ __global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_ke
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) o[n][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
-
-        // A tile's scores y of the lane's tokens tok .. tok + 8, and where their values are.
-        auto scores = [&](int t0, int p0, int p1, float (&y)[NT][8], V& v, const char*& va) {
-            u32x4_t k[2][Q::STEPS];
-            const int tk = t0 + 8 * (c >> 2) + (c & 3), tok = t0 + 8 * g;
-            const int pk = (c >> 2) & 2 ? p1 : p0, pv = g & 2 ? p1 : p0;
-            const char* ka = (const char*)a.c.k + ((((int64_t)max(pk, 0) * H + h) * P + (tk & (P - 1))) * D) * ES + 16 * g;
+        // A tile's scores y of the lane's tokens tok .. tok + 8.
+        auto scores = [&](int t0, int p0, int p1, float (&y)[NT][8]) {
+            const int tok = t0 + 8 * g;
+            if (SHARES) asm volatile("" : "+v"(low));  // keeps the low parts where they are: registers are full
+            f32x4_t s[2][NT];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int n = 0; n < NT; ++n) s[0][n] = s[1][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < Q::STEPS; ++s) k[mt][s] = *(const u32x4_t*)(ka + 4 * mt * D * ES + 64 * s);
-            va = (const char*)a.c.v + ((((int64_t)max(pv, 0) * H + h) * P + (tok & (P - 1))) * D + 4 * c) * ES;
-            v.load(va, D * ES);
+            for (int st = 0; st < Keys<BF16, D>::STEPS; ++st) {
+                const u32x4_t x[2] = {k.step(0, st), k.step(1, st)};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) q[n].template times<NT>(x, st, s_low + low + n * 64, s[0][n], s[1][n]);
+                if (SHARES) __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    const f32x4_t s = q[n].times(k[mt]);
+                for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[n][4 * mt + i] = s[i] * y2;
-                }
+                    for (int i = 0; i < 4; ++i) y[n][4 * mt + i] = s[mt][n][i] * y2;
             if ((p0 | p1) < 0) {  // a page out of range
+                const bool lost = (g & 2 ? p1 : p0) < 0;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[n][e] = pv < 0 ? nan32() : y[n][e];
+                    for (int e = 0; e < 8; ++e) y[n][e] = lost ? nan32() : y[n][e];
             }
             if (t0 + kTile > first_end) {
 #pragma unroll
@@ -386,14 +555,12 @@ __global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_ke
             }
         };
         bool apart = false;
-        for (; tile < t_end; tile += kWaves) {
+        for (; tile < t_end; tile += W) {
             const int t0 = tile * kTile, tok = t0 + 8 * g;
             float y[NT][8], top[NT];
-            V v;
-            const char* va;
-            const int at0 = p0, at1 = p1;
-            if (tile + kWaves < t_end) p0 = page_of(tile + kWaves, 0), p1 = page_of(tile + kWaves, 1);
-            scores(t0, at0, at1, y, v, va);
+            load_keys(t0, p0, p1);
+            v.template load<STREAM>(values_at(t0, p0, p1), D * ES);
+            scores(t0, p0, p1, y);
             bool move = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -430,10 +597,7 @@ __global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_ke
             if (t0 + kTile > first_end) {
                 // Values past the sequence's end may be anything: they become zeros, since 0 times NaN is NaN.  Where one
                 // that only some of the rows see is not finite, the tile is multiplied after the loop, query by query.
-                bool odd = false;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) odd |= tok + e >= first_end && tok + e < len && !v.finite(e);
-                const bool later = __any(odd);
+                const bool later = __any(odd(v, first_end - tok, len - tok));
                 apart |= later;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v.keep(e, tok + e < len && !later);
@@ -442,53 +606,12 @@ __global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_ke
             for (int t = 0; t < D / 16; ++t)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) o[n][t] = v.times(t >> 2, t & 3, w[n], o[n][t]);
+            p0 = n0, p1 = n1;
+            if (tile + 2 * W < t_end) n0 = page_of(tile + 2 * W, 0), n1 = page_of(tile + 2 * W, 1);
         }
-        if (apart) {
-            for (int t1 = t_begin + wave; t1 < t_end; t1 += kWaves) {
-                const int t0 = t1 * kTile, tok = t0 + 8 * g;
-                if (t0 + kTile <= first_end) continue;
-                float y[NT][8];
-                V v;
-                const char* va;
-                scores(t0, page_of(t1, 0), page_of(t1, 1), y, v, va);
-                bool odd = false;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) odd |= tok + e >= first_end && tok + e < len && !v.finite(e);
-                if (!__any(odd)) continue;
-                Weights w[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[n][e] = __builtin_amdgcn_exp2f(y[n][e] - m[n]);
-                    w[n].set(y[n]);
-                }
-                for (int hf = 0; hf < D / 64; ++hf) {
-                    Values<BF16, 64> x;
-                    x.load(va + 64 * ES * hf, D * ES);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            f32x4_t before = o[n][j], sum;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) sum[i] = before[i] = hf ? o[n][D / 16 - 4 + j][i] : before[i];
-#pragma unroll 1
-                            for (int upto = first_end; upto <= len; ++upto) {
-                                const f32x4_t by = x.times_first(0, j, upto - tok, w[n], before);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) sum[i] = end[n] == upto ? by[i] : sum[i];
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                o[n][j][i] = hf ? o[n][j][i] : sum[i];
-                                o[n][D / 16 - 4 + j][i] = hf == D / 64 - 1 ? sum[i] : o[n][D / 16 - 4 + j][i];
-                            }
-                        }
-                }
-            }
-        }
-
         // join the waves: a fixed order, so the result does not depend on who is first
+        asm volatile("" : "+v"(tid));  // (nor across the loop above)
+        const int row0 = tid & 15, dim0 = (tid & 63) >> 4 << 4;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             double t = l[n];
@@ -496,9 +619,9 @@ __global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_ke
             t += __shfl_xor(t, 32);
             float lf;
             const int down = settle_sum(t, m[n], lf);
-            if (g == 0) {
-                s_ml[wave][n * 16 + c][0] = m[n];
-                s_ml[wave][n * 16 + c][1] = lf;
+            if (dim0 == 0) {
+                s_ml[wave][n * 16 + row0][0] = m[n];
+                s_ml[wave][n * 16 + row0][1] = lf;
             }
 #pragma unroll
             for (int hf = 0; hf < D / 64; ++hf)
@@ -507,22 +630,54 @@ __global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_ke
                     f32x4_t x;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[j] = __builtin_amdgcn_ldexpf(o[n][4 * hf + j][i], down);
-                    *(f32x4_t*)&s_o[wave][n * 16 + c][64 * hf + 16 * g + 4 * i] = x;
+                    *(f32x4_t*)&s_o[wave][n * 16 + row0][64 * hf + dim0 + 4 * i] = x;
                 }
         }
-        if (tid == 255 && cuts && s_begin == 0) {  // (of several items that begin here only the last may be cut)
-            const int pieces = (int)div64(item_at + steps - 1, share) - (int)blockIdx.x + 1, id = b * items + item;
-            sp.cut[sp.few ? id : (int)blockIdx.x] = make_int2(sp.few ? (int)blockIdx.x : id, pieces);
+        if (apart) {
+            // The tiles left out above, query by query, each with what it sees, onto the wave's sums where they are now.
+            for (int t1 = t_begin + wave; t1 < t_end; t1 += W) {
+                const int t0 = t1 * kTile, tok = t0 + 8 * g;
+                if (t0 + kTile <= first_end) continue;
+                p0 = page_of(t1, 0), p1 = page_of(t1, 1);
+                const char* va = values_at(t0, p0, p1);
+                v.template load<false>(va, D * ES);
+                if (!__any(odd(v, first_end - tok, len - tok))) continue;
+                load_keys(t0, p0, p1);
+                float y[NT][8];
+                scores(t0, p0, p1, y);
+                Weights w[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[n][e] = __builtin_amdgcn_exp2f(y[n][e] - m[n]);
+                    w[n].set(y[n]);
+                }
+                for (int upto = first_end; upto <= len; ++upto)
+#pragma unroll
+                    for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const f32x4_t by = v.times_first(t >> 2, t & 3, upto - tok, w[n], f32x4_t{0.f, 0.f, 0.f, 0.f});
+                            float* to = &s_o[wave][n * 16 + row0][64 * (t >> 2) + dim0 + (t & 3)];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (end[n] == upto) to[4 * i] += by[i];
+                        }
+            }
+        }
+        if (tid == THREADS - 1 && cuts && s_begin == 0) {  // (of several items that begin here only the last may be cut)
+            const int pieces = (int)div64(item_at + steps - 1, share) - (int)piece + 1, id = b * items + item;
+            sp.cut[sp.few ? id : (int)piece] = make_int2(sp.few ? (int)piece : id, pieces);
         }
         __syncthreads();
         const int rows = min(ROWS, R - rb * ROWS);
         const bool part = s_begin > 0 || s_end < steps;
-        const int64_t slot = q8_slot(blockIdx.x, s_begin == 0) * ROWS;
-        for (int x = tid; x < rows * (D / 4); x += 256) {
+        const int64_t slot = q8_slot(piece, s_begin == 0) * ROWS;
+        for (int x = tid; x < rows * (D / 4); x += THREADS) {
             const int row = x / (D / 4), d4 = x % (D / 4) * 4;
             float top, lsum;
             f32x4_t sum;
-            join_waves<ROWS, LDO>(s_o, s_ml, row, d4, top, lsum, sum);
+            join_own<W, ROWS, LDO>(s_o, s_ml, row, d4, top, lsum, sum);
             if (part) {
                 *(f32x4_t*)(sp.part_o + (slot + row) * D + d4) = sum;
                 if (d4 == 0) *(float2*)(sp.part_ml + (slot + row) * 2) = make_float2(top, lsum);
@@ -539,42 +694,46 @@ __global__ __launch_bounds__(256, (per_cu(BF16, NT, TURN))) void paged_decode_ke
 
 }  // namespace
 
-// Sequences of at most this many steps are never cut: a workgroup's further steps cost less than the joining kernel.
-constexpr int kWhole = 4;
+// Sequences of at most this many tokens are not cut: a workgroup's further steps cost less than the joining kernel; and of
+// at most kFull where there is an item for every CU.
+constexpr int kWhole = 256, kFull = 768;
 
-Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int max_len, bool turn, int cus) {
+Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, bool turn, int cus) {
     Q8Plan p{};
+    const bool bf16 = e == Elem::BF16;
     const int64_t R = (int64_t)n_q * (Hq / H);
     const int nt = R <= 16 ? 1 : 2;  // 16-row tiles of a workgroup
     p.rows = 16 * nt;
     p.row_blocks = (int)((R + p.rows - 1) / p.rows);
+    p.waves = waves_of(bf16, d, nt, turn);
     const double items = (double)B * H * p.row_blocks;
-    const int steps = paged_steps(max_len, max_len);
-    p.splits = steps > kWhole;
+    p.splits = max_len > (items < cus ? kWhole : kFull);
     // a workgroup for every step that the lengths can bring, up to what the chip holds at once
-    p.grid = (int)std::min<double>((double)per_cu(e == Elem::BF16, nt, turn) * cus, p.splits ? items * steps : items);
+    const int steps = steps_of(max_len, max_len, kTile * p.waves);
+    p.grid = (int)std::min<double>((double)(4 * per_simd(bf16, d, nt, turn) / p.waves) * cus, p.splits ? items * steps : items);
     return p;
 }
 
-template <bool BF16, int D, bool TURN>
-static hipError_t launch_decode(const Q8Attend& a, const Rotation& rot, const Q8Pieces& sp, hipStream_t s) {
-    const dim3 grid((unsigned)sp.grid);
-    if (sp.rows == 16) hipLaunchKernelGGL((paged_decode_kernel<BF16, D, 1, TURN>), grid, dim3(256), 0, s, a, rot, sp);
-    else hipLaunchKernelGGL((paged_decode_kernel<BF16, D, 2, TURN>), grid, dim3(256), 0, s, a, rot, sp);
+template <bool BF16, int D, int NT, bool TURN>
+static hipError_t launch_decode(const Q8Attend& a, const Rotation& rot, const Q8Pieces& sp, const Q8Plan& p, hipStream_t s) {
+    constexpr int W = waves_of(BF16, D, NT, TURN);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)p.grid), dim3(64 * W), 0, s, a, rot, sp); };
+    if (NT == 2 && p.row_blocks > 1) go(paged_decode_kernel<BF16, D, 2, TURN, false, W>);
+    else go(paged_decode_kernel<BF16, D, NT, TURN, true, W>);
     return hipGetLastError();
+}
+
+template <bool BF16, int D>
+static hipError_t launch_of(const Q8Attend& a, const Rotation& rot, const Q8Pieces& sp, const Q8Plan& p, hipStream_t s) {
+    if (rot.tab) return p.rows == 16 ? launch_decode<BF16, D, 1, true>(a, rot, sp, p, s) : launch_decode<BF16, D, 2, true>(a, rot, sp, p, s);
+    return p.rows == 16 ? launch_decode<BF16, D, 1, false>(a, rot, sp, p, s) : launch_decode<BF16, D, 2, false>(a, rot, sp, p, s);
 }
 
 hipError_t launch_paged_attend(Elem e, const Q8Attend& a, const Rotation& rot, const Q8Plan& p, void* scratch, hipStream_t s) {
     const Q8Pieces sp = q8_pieces(a, p, scratch);
-    const bool bf16 = e == Elem::BF16, wide = a.c.d == 128;
     hipError_t r;
-    if (rot.tab) {
-        if (bf16) r = wide ? launch_decode<true, 128, true>(a, rot, sp, s) : launch_decode<true, 64, true>(a, rot, sp, s);
-        else r = wide ? launch_decode<false, 128, true>(a, rot, sp, s) : launch_decode<false, 64, true>(a, rot, sp, s);
-    } else {
-        if (bf16) r = wide ? launch_decode<true, 128, false>(a, rot, sp, s) : launch_decode<true, 64, false>(a, rot, sp, s);
-        else r = wide ? launch_decode<false, 128, false>(a, rot, sp, s) : launch_decode<false, 64, false>(a, rot, sp, s);
-    }
+    if (e == Elem::BF16) r = a.c.d == 128 ? launch_of<true, 128>(a, rot, sp, p, s) : launch_of<true, 64>(a, rot, sp, p, s);
+    else r = a.c.d == 128 ? launch_of<false, 128>(a, rot, sp, p, s) : launch_of<false, 64>(a, rot, sp, p, s);
     return r == hipSuccess && p.splits ? launch_q8_join(e, a, sp, s) : r;
 }
 

@@ -73,8 +73,4 @@ KVMAP_HD Q8Cut q8_cut(uint64_t at, int tiles, uint64_t share, uint64_t w) {
 constexpr int kQ8Step = 256;
 KVMAP_HD int steps_of(int len, int max_len, int step) { return len < 1 || len > max_len ? 1 : (len - 1) / step + 1; }
 KVMAP_HD int q8_steps(int len, int max_len) { return steps_of(len, max_len, kQ8Step); }
-// Over the cache in the model's own type, whose tokens are twice and four times as many bytes.
-constexpr int kPagedStep = 128;
-KVMAP_HD int paged_steps(int len, int max_len) { return steps_of(len, max_len, kPagedStep); }
-
 }  // namespace kvmap
