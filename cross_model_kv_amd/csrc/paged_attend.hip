@@ -61,13 +61,6 @@ struct Queries<true, D, TURN> {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) t[4 * s + e] = *(const f32x4_t*)(tab + 32 * s + 8 * g + 2 * e);
     }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) p[s] = bf16x8_t{};
-        if (TURN)
-#pragma unroll
-            for (int s = 0; s < STEPS * 2; ++s) t[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
     template <int N>
     __device__ __forceinline__ void ready(u32x4_t* low, bool write) {
         if (!TURN) return;
@@ -131,13 +124,6 @@ struct Queries<false, D, TURN> {
             for (int s = 0; s < STEPS / 2; ++s)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) t[2 * s + e] = *(const f32x4_t*)(tab + 16 * s + 4 * g + 2 * e);
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) p[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        if (TURN)
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) t[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
     template <int N>
     __device__ __forceinline__ void ready(u32x4_t*, bool) {
@@ -344,6 +330,13 @@ __device__ __forceinline__ bool odd(const V& v, int from, int to) {
     return any;
 }
 
+// One value at an address that all lanes share and no workgroup writes, through the scalar cache.
+template <class T>
+__device__ __forceinline__ T uniform(const T* p) {
+    typedef const T __attribute__((address_space(4))) * constant_ptr;
+    return *(constant_ptr)(uintptr_t)p;
+}
+
 // Waves that a SIMD holds at once, as the registers allow.
 __host__ __device__ constexpr int per_simd(bool bf16, int d, int nt, bool turn) {
     if (d == 64) return nt == 2 ? 2 : bf16 ? 4 : 3;
@@ -388,89 +381,100 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT, TURN))) void paged_d
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int H = a.c.H, G = a.Hq / H, R = a.n_q * G;
     const int P = a.c.page, logP = 31 - __clz(P);
-    const int items = H * sp.row_blocks;  // of one sequence
+    const int rbs = sp.row_blocks;
     const float y2 = a.scale * kLog2e;
     const bool cuts = sp.cut != nullptr;
     const int lane0 = threadIdx.x & 63;
-    // Where items may be cut: this workgroup's piece [at, stop) of the line of steps, and the sequence that it begins in.
-    // Else whole items, one after the other.
-    uint64_t stop = (uint64_t)a.B * items, share = 1, base = 0;
+    // Where items may be cut: this workgroup's piece [at, stop) of the line of steps of all (sequence, KV head), the sequence that
+    // it begins in, and its block of rows: the blocks of a piece are neighbours, and find what they share in the caches.
+    // Else one whole item.
+    const int pieces = gridDim.x / rbs;
+    uint64_t stop = 0, share = 1, base = 0;
     uint32_t upto = 0, used = gridDim.x;
     int b = 0;
     if (cuts) {
         upto = steps_upto(a, 0, STEP, lane0);
         uint64_t total = lane_value(upto, 63);
         for (int b0 = 64; b0 < a.B; b0 += 64) total += lane_value(steps_upto(a, b0, STEP, lane0), 63);
-        stop = total *= items;
-        share = div64(total + gridDim.x - 1, gridDim.x);
-        if (4 * per_simd(BF16, D, NT, TURN) / W == 3 && gridDim.x % 3 == 0) {
-            const uint64_t two = gridDim.x / 3 * 2, share2 = div64(total + two - 1, two);
+        stop = total *= H;
+        share = div64(total + pieces - 1, pieces);
+        if (4 * per_simd(BF16, D, NT, TURN) / W == 3 && pieces % 3 == 0) {
+            // Of three workgroups a CU the third may go where the steps divide better by two (8 sequences of 8,192 tokens 60 us,
+            // by three 64; with the same number of steps a CU three are up to 5 % faster).
+            const uint64_t two = pieces / 3 * 2, share2 = div64(total + two - 1, two);
             if (34 * share2 < 48 * share) share = share2;
         }
-        used = (uint32_t)div64(total + share - 1, share);
-        if (blockIdx.x >= used) {
-            if (threadIdx.x == 0 && !sp.few) sp.cut[blockIdx.x] = make_int2(0, 1);
+        used = (uint32_t)div64(total + share - 1, share) * rbs;
+        if (blockIdx.x >= used) {  // a piece of nothing
+            const int j = blockIdx.x - used;
+            if (threadIdx.x == 0 && !sp.few) sp.cut[j % rbs * pieces + used / rbs + j / rbs] = make_int2(0, 1);
             return;
         }
     }
-    // neighbouring pieces on one XCD (workgroups go round the 8 XCDs), so that the heads of a page meet in its caches
-    const uint32_t xcd = blockIdx.x % 8, piece = xcd * (used / 8) + min(xcd, used % 8) + blockIdx.x / 8;
-    uint64_t at = share * piece;
+    // neighbours on one XCD (workgroups go round the 8 XCDs), so that the heads of a page meet in its caches
+    const uint32_t xcd = blockIdx.x % 8, place = xcd * (used / 8) + min(xcd, used % 8) + blockIdx.x / 8;
+    const int rb = place % rbs, piece = rb * pieces + place / rbs;  // (pieces of one block of rows are numbered in order)
+    uint64_t at = share * (place / rbs);
     if (cuts) {
         stop = min(stop, at + share);
         if (threadIdx.x == THREADS - 1 && !sp.few) sp.cut[piece] = make_int2(0, 1);  // (by the thread that may write it again)
         for (int b0 = 0;;) {
-            const uint64_t past = __ballot(base + (uint64_t)upto * items > at);
+            const uint64_t past = __ballot(base + (uint64_t)upto * H > at);
             if (past) {
                 const int n = __ffsll((unsigned long long)past) - 1;
                 b = b0 + n;
-                if (n) base += (uint64_t)lane_value(upto, n - 1) * items;
+                if (n) base += (uint64_t)lane_value(upto, n - 1) * H;
                 break;
             }
-            base += (uint64_t)lane_value(upto, 63) * items;
+            base += (uint64_t)lane_value(upto, 63) * H;
             b0 += 64;
             if (b0 >= a.B) return;  // (not reached while the lengths stay as they were summed)
             upto = steps_upto(a, b0, STEP, lane0);
         }
+    } else {
+        b = (int)at / H;
+        stop = at + 1;
     }
 
     while (at < stop) {
-        int item, steps, s_begin = 0, s_end;  // the item of sequence b, and its steps that are this workgroup's
-        uint64_t item_at = 0;
+        int h, steps, s_begin = 0, s_end;  // the head of sequence b, and its steps that are this workgroup's
+        uint64_t item_at = at;
+        b = __builtin_amdgcn_readfirstlane(b);
+        const int len = uniform(a.len + b);
+        steps = steps_of(len, a.max_len, STEP);
         if (cuts) {
-            b = __builtin_amdgcn_readfirstlane(b);
-            steps = steps_of(a.len[b], a.max_len, STEP);
-            const uint64_t next = base + (uint64_t)steps * items;
+            const uint64_t next = base + (uint64_t)steps * H;
             if (at >= next) {
                 base = next;
                 if (++b >= a.B) return;  // (as above)
                 continue;
             }
-            item = (int)div64(at - base, steps);
-            item_at = base + (uint64_t)item * steps;
+            h = (int)div64(at - base, steps);
+            item_at = base + (uint64_t)h * steps;
             s_begin = (int)(at - item_at);
             s_end = (int)min((uint64_t)steps, stop - item_at);
         } else {
-            b = __builtin_amdgcn_readfirstlane((int)((uint32_t)at / (uint32_t)items));
-            item = (int)((uint32_t)at - (uint32_t)b * (uint32_t)items);
-            s_end = steps = steps_of(a.len[b], a.max_len, STEP);
+            h = (int)at - b * H;
+            s_end = steps;
         }
-        item = __builtin_amdgcn_readfirstlane(item);
+        h = __builtin_amdgcn_readfirstlane(h);
         int tid = threadIdx.x;
         asm volatile("" : "+v"(tid));  // keeps products of it with strides from being held across items: registers are full
         const int lane = tid & 63, c = lane & 15, g = lane >> 4;
-        const int len = a.len[b];
         const bool bad = len < 0 || len > a.max_len;
         const int tiles = bad ? 0 : (len + kTile - 1) / kTile;
-        const int h = item / sp.row_blocks, rb = item - h * sp.row_blocks;
         const int t_begin = s_begin * W, t_end = min(tiles, s_end * W);
 
         const int32_t* pages = a.pages + (int64_t)b * a.max_pages;
         // the pages of a tile's first and last 16 tokens
-        auto page_of = [&](int tile, int half) { return q8_page_at(pages, (int64_t)(tile * kTile + 16 * half) >> logP, a.max_pages, a.c.n_pages); };
+        auto page_of = [&](int tile, int half) {
+            const int slot = (int)((int64_t)(tile * kTile + 16 * half) >> logP);
+            if (slot >= a.max_pages) return -1;
+            const int page = uniform(pages + slot);
+            return page >= 0 && page < a.c.n_pages ? page : -1;
+        };
         int tile = t_begin + wave;
-        int p0 = -1, p1 = -1, n0 = -1, n1 = -1;  // of the tile in hand, and of the next one
-        if (tile < t_end) p0 = page_of(tile, 0), p1 = page_of(tile, 1);
+        int p0 = page_of(tile, 0), p1 = page_of(tile, 1), n0 = -1, n1 = -1;  // of the tile in hand, and of the next one
 
         // this lane's rows: their queries, and the tokens that they see
         Q q[NT];
@@ -478,17 +482,12 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT, TURN))) void paged_d
         const int first_end = len - a.n_q + 1;  // the fewest tokens that a row sees
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = rb * ROWS + n * 16 + c;
-            const int i = q8_query(a, r);
+            const int r = min(rb * ROWS + n * 16 + c, R - 1);  // (rows past the last are not stored)
+            const int i = q8_query(a, r), hq = h * G + r - i * G;
             end[n] = first_end + i;
-            const int pos = first_end + i - 1;
-            if (r < R && pos >= 0 && !bad) {
-                const int hq = h * G + r - i * G;
-                q[n].load((const char*)a.q.base + ((int64_t)b * a.q.seq + (int64_t)hq * a.q.head + (int64_t)i * a.q.token) * ES, g,
-                          TURN ? rot.tab + (int64_t)pos * (D / 2) : nullptr);
-            } else {
-                q[n].zero();
-            }
+            const int pos = bad ? 0 : max(end[n] - 1, 0);
+            q[n].load((const char*)a.q.base + ((int64_t)b * a.q.seq + (int64_t)hq * a.q.head + (int64_t)i * a.q.token) * ES, g,
+                      TURN ? rot.tab + (int64_t)pos * (D / 2) : nullptr);
         }
         // A tile's keys and values.  A lane's 8 tokens of values lie in one page, which has whole 16 tokens, and so do the rows of
         // keys of one load.  What one workgroup alone reads is read past the caches (STREAM).
@@ -666,8 +665,8 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT, TURN))) void paged_d
             }
         }
         if (tid == THREADS - 1 && cuts && s_begin == 0) {  // (of several items that begin here only the last may be cut)
-            const int pieces = (int)div64(item_at + steps - 1, share) - (int)piece + 1, id = b * items + item;
-            sp.cut[sp.few ? id : (int)piece] = make_int2(sp.few ? (int)piece : id, pieces);
+            const int n = (int)div64(item_at + steps - 1, share) - place / rbs + 1, id = (b * H + h) * rbs + rb;
+            sp.cut[sp.few ? id : piece] = make_int2(sp.few ? piece : id, n);
         }
         __syncthreads();
         const int rows = min(ROWS, R - rb * ROWS);
@@ -687,16 +686,18 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT, TURN))) void paged_d
                 q8_store_row<BF16>(a, b, i, h * G + r - i * G, d4, top, lsum, sum);
             }
         }
-        at = cuts ? item_at + s_end : at + gridDim.x;
+        at = item_at + s_end;
         __syncthreads();  // the next item's sums come into the same memory
     }
 }
 
 }  // namespace
 
-// Sequences of at most this many tokens are not cut: a workgroup's further steps cost less than the joining kernel; and of
-// at most kFull where there is an item for every CU.
-constexpr int kWhole = 256, kFull = 768;
+// Items of sequences of at most this many tokens are not cut, each a workgroup's that the chip takes up as others end: where there
+// are few of them a workgroup's second step costs less than the joining kernel (130 tokens of one sequence 7.2 us, cut 9.1; 512:
+// 14.7, cut 10.0); with one for every CU (32 sequences of 1,000, 8 heads: 28 us, cut 33); with one for every workgroup
+// that the chip holds (128 of 1,500: 133, cut 144; 64 of up to 1,400: 42 and 48; with 256 items for 512 places, fp32: 37 and 28).
+constexpr int kWhole = 256, kFull = 1024, kMany = 2048;
 
 Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, bool turn, int cus) {
     Q8Plan p{};
@@ -707,10 +708,10 @@ Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_l
     p.row_blocks = (int)((R + p.rows - 1) / p.rows);
     p.waves = waves_of(bf16, d, nt, turn);
     const double items = (double)B * H * p.row_blocks;
-    p.splits = max_len > (items < cus ? kWhole : kFull);
-    // a workgroup for every step that the lengths can bring, up to what the chip holds at once
-    const int steps = steps_of(max_len, max_len, kTile * p.waves);
-    p.grid = (int)std::min<double>((double)(4 * per_simd(bf16, d, nt, turn) / p.waves) * cus, p.splits ? items * steps : items);
+    const int steps = steps_of(max_len, max_len, kTile * p.waves), held = 4 * per_simd(bf16, d, nt, turn) / p.waves * cus;
+    p.splits = max_len > (items < cus ? kWhole : items < held ? kFull : kMany) && held / p.row_blocks > 1;
+    // cut: a workgroup for every step that the lengths can bring, up to what the chip holds at once; else one for every item
+    p.grid = p.splits ? (int)std::min<double>(held / p.row_blocks, (double)B * H * steps) * p.row_blocks : (int)items;
     return p;
 }
 
