@@ -205,7 +205,6 @@ struct Q8Plan {
     int grid;              // workgroups
     bool splits;           // items may be cut: scratch and a second kernel
     bool prompt;           // many rows: q8_prompt.hip's kernel
-    int waves;             // of a workgroup (paged_attend.hip)
 };
 // Work is dealt out in steps of some tokens.  The steps of all items (sequence, KV head, row block), an item's own in
 // order, are one line of which every workgroup takes an equal piece: unequal lengths keep every CU busy, and the
@@ -258,7 +257,7 @@ hipError_t launch_paged_read(Elem e, const PagedPools& c, const Q8Seqs& q, int n
                              const Q8Rows& v, const Rotation& rot, hipStream_t s);
 // a.c: k and v are one layer's pools, its scales are not used; work is dealt out, and pieces are joined through the scratch, as
 // the 8-bit cache's are.
-Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, bool turn, int cus);
+Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus);
 hipError_t launch_paged_attend(Elem e, const Q8Attend& a, const Rotation& rot, const Q8Plan& p, void* scratch, hipStream_t s);
 
 // Error reporting shared by the C-ABI files: sets the calling thread's last-error string.

@@ -232,7 +232,7 @@ extern "C" int kvmap_paged_attend(kvmap_ctx* ctx, const kvmap_paged_cache* c, in
     Q8Attend a{{(uint8_t*)p.k, (uint8_t*)p.v, nullptr, nullptr, 0, 0, p.n_pages, p.H, p.page, p.d}, pages, len, B, n_q, H_q,
                max_pages, max_len, (float)scale, rows(q), rows(out), lse, 0, 0};
     q8_divisor((uint32_t)(H_q / c->H_kv), a.g_mul, a.g_shift);
-    const Q8Plan plan = paged_attend_plan(elem(c), B, n_q, H_q, c->H_kv, c->head_dim, max_len, rot != nullptr, s->cus);
+    const Q8Plan plan = paged_attend_plan(elem(c), B, n_q, H_q, c->H_kv, c->head_dim, max_len, s->cus);
     if (plan.splits) {
         const int r = ensure_scratch(s, (hipStream_t)stream, true, "kvmap_paged");
         if (r) return r;

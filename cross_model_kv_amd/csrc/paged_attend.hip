@@ -20,6 +20,14 @@
 // bf16 calls: weights as two bf16 parts (16 bits, fp32's exponents: a weight counts however far below the row's largest
 // it lies), queries that were turned as three (24 bits, what their turn in fp32 has).  fp32 calls: products of fp32
 // operands.  Sums and statistics in fp32, a row's sum of weights in fp64.
+//
+// What bounds it: bytes, where there are enough of them.  Keys and values are read once, past the caches and by whole lines of
+// 128 bytes, a tile's 16 KB at a time by each of 8 waves a CU: 64 sequences of 8,192 tokens, 8 KV heads, 2.15 GB in 339 us, 6.35 TB/s
+// (loads alone in the same pattern 6.8; through the caches 5.3), of up to 16,384 in 333, one of 32,768 134 MB in 27 and 4 to
+// join (loads alone 23).  Asking for a tile's keys while the one before is multiplied was no faster, with registers for two
+// tiles or with the keys' alone.  Below some thousand tokens a sequence it is the way through one step: lengths, pages, keys, the tile's
+// products and the joining of the waves one after the other, 7.2 us for 130 tokens.  Pieces are joined by a second kernel: by the last
+// piece to come, through memory past the caches, it took 58 us for 38 on one sequence of 32,768 tokens and 63 for 61 on 8 of 8,192.
 
 #include <algorithm>
 #include <type_traits>
@@ -337,13 +345,14 @@ __device__ __forceinline__ T uniform(const T* p) {
     return *(constant_ptr)(uintptr_t)p;
 }
 
-// Waves that a SIMD holds at once, as the registers allow.
-__host__ __device__ constexpr int per_simd(bool bf16, int d, int nt, bool turn) {
-    if (d == 64) return nt == 2 ? 2 : bf16 ? 4 : 3;
-    return nt == 2 ? (bf16 ? 2 : 1) : bf16 && !turn ? 3 : 2;
+// Waves that a SIMD holds at once, as the registers allow; bf16 rows of 128 dims would fit three times in 16-row tiles, but steps divide
+// better by two, and two have enough in flight (64 sequences of 8,192 tokens 345 us, three 366).
+__host__ __device__ constexpr int per_simd(bool bf16, int d, int nt) {
+    if (d == 64) return nt == 2 ? 2 : 4;
+    return nt == 2 && !bf16 ? 1 : 2;
 }
-// Waves of a workgroup.
-__host__ __device__ constexpr int waves_of(bool bf16, int d, int nt, bool turn) { return nt == 2 && per_simd(bf16, d, nt, turn) > 1 ? 8 : 4; }
+// Waves of a workgroup.  With two row tiles all of a CU's: the low parts of the queries then lie in its shared memory once.
+__host__ __device__ constexpr int waves_of(bool bf16, int d, int nt) { return nt == 2 && per_simd(bf16, d, nt) > 1 ? 8 : 4; }
 
 // Steps of one item of each of 64 sequences, summed up to and including the lane's.
 __device__ __forceinline__ uint32_t steps_upto(const Q8Attend& a, int b0, int step, int lane) {
@@ -368,7 +377,7 @@ __device__ __forceinline__ void join_own(const float (*o)[ROWS][LDO], const floa
 }
 
 template <bool BF16, int D, int NT, bool TURN, bool STREAM, int W>
-__global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT, TURN))) void paged_decode_kernel(Q8Attend a, Rotation rot, Q8Pieces sp) {
+__global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT))) void paged_decode_kernel(Q8Attend a, Rotation rot, Q8Pieces sp) {
     constexpr int ROWS = 16 * NT, ES = BF16 ? 2 : 4, LDO = D + 4, THREADS = 64 * W, STEP = kTile * W;
     constexpr bool SHARES = BF16 && TURN && NT >= kShared;
     constexpr int LOW = SHARES ? 2 * (D / 32) * NT * 64 : 1;
@@ -398,12 +407,6 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT, TURN))) void paged_d
         for (int b0 = 64; b0 < a.B; b0 += 64) total += lane_value(steps_upto(a, b0, STEP, lane0), 63);
         stop = total *= H;
         share = div64(total + pieces - 1, pieces);
-        if (4 * per_simd(BF16, D, NT, TURN) / W == 3 && pieces % 3 == 0) {
-            // Of three workgroups a CU the third may go where the steps divide better by two (8 sequences of 8,192 tokens 60 us,
-            // by three 64; with the same number of steps a CU three are up to 5 % faster).
-            const uint64_t two = pieces / 3 * 2, share2 = div64(total + two - 1, two);
-            if (34 * share2 < 48 * share) share = share2;
-        }
         used = (uint32_t)div64(total + share - 1, share) * rbs;
         if (blockIdx.x >= used) {  // a piece of nothing
             const int j = blockIdx.x - used;
@@ -699,16 +702,16 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT, TURN))) void paged_d
 // that the chip holds (128 of 1,500: 133, cut 144; 64 of up to 1,400: 42 and 48; with 256 items for 512 places, fp32: 37 and 28).
 constexpr int kWhole = 256, kFull = 1024, kMany = 2048;
 
-Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, bool turn, int cus) {
+Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus) {
     Q8Plan p{};
     const bool bf16 = e == Elem::BF16;
     const int64_t R = (int64_t)n_q * (Hq / H);
     const int nt = R <= 16 ? 1 : 2;  // 16-row tiles of a workgroup
     p.rows = 16 * nt;
     p.row_blocks = (int)((R + p.rows - 1) / p.rows);
-    p.waves = waves_of(bf16, d, nt, turn);
     const double items = (double)B * H * p.row_blocks;
-    const int steps = steps_of(max_len, max_len, kTile * p.waves), held = 4 * per_simd(bf16, d, nt, turn) / p.waves * cus;
+    const int waves = waves_of(bf16, d, nt);
+    const int steps = steps_of(max_len, max_len, kTile * waves), held = 4 * per_simd(bf16, d, nt) / waves * cus;
     p.splits = max_len > (items < cus ? kWhole : items < held ? kFull : kMany) && held / p.row_blocks > 1;
     // cut: a workgroup for every step that the lengths can bring, up to what the chip holds at once; else one for every item
     p.grid = p.splits ? (int)std::min<double>(held / p.row_blocks, (double)B * H * steps) * p.row_blocks : (int)items;
@@ -717,10 +720,14 @@ Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_l
 
 template <bool BF16, int D, int NT, bool TURN>
 static hipError_t launch_decode(const Q8Attend& a, const Rotation& rot, const Q8Pieces& sp, const Q8Plan& p, hipStream_t s) {
-    constexpr int W = waves_of(BF16, D, NT, TURN);
+    constexpr int W = waves_of(BF16, D, NT);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)p.grid), dim3(64 * W), 0, s, a, rot, sp); };
-    if (NT == 2 && p.row_blocks > 1) go(paged_decode_kernel<BF16, D, 2, TURN, false, W>);
-    else go(paged_decode_kernel<BF16, D, NT, TURN, true, W>);
+    if constexpr (NT == 2)
+        if (p.row_blocks > 1) {
+            go(paged_decode_kernel<BF16, D, NT, TURN, false, W>);
+            return hipGetLastError();
+        }
+    go(paged_decode_kernel<BF16, D, NT, TURN, true, W>);
     return hipGetLastError();
 }
 
