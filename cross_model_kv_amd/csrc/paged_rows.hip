@@ -72,27 +72,27 @@ struct Token {
     bool live;     // belongs to the sequence's count
     bool bad_seq;  // start or count out of range
 };
-__device__ __forceinline__ Token token_of(const Q8Seqs& q, int n, int64_t t, int n_pages, int P, const Rotation& rot) {
+__device__ __forceinline__ Token token_of(const Q8Seqs& q, uint32_t n, uint32_t t, int n_pages, int P, const Rotation& rot) {
     Token x;
     x.b = (int)(t / n);
-    x.i = (int)(t - (int64_t)x.b * n);
-    const int start = q.start[x.b], count = q.count ? q.count[x.b] : n;
-    x.bad_seq = start < 0 || count < 0 || count > n;
+    x.i = (int)(t - (uint32_t)x.b * n);
+    const int start = q.start[x.b], count = q.count ? q.count[x.b] : (int)n;
+    x.bad_seq = start < 0 || count < 0 || count > (int)n;
     x.pos = (int64_t)start + x.i;
     x.live = x.bad_seq || x.i < count;
     const bool there = x.live && !x.bad_seq && (!rot.tab || x.pos < rot.n_pos);
-    x.page = there ? q8_page_at(q.pages + (int64_t)x.b * q.max_pages, x.pos / P, q.max_pages, n_pages) : -1;
+    x.page = there ? q8_page_at(q.pages + (int64_t)x.b * q.max_pages, x.pos >> (31 - __clz(P)), q.max_pages, n_pages) : -1;
     x.row = (int)(x.pos & (P - 1));
     return x;
 }
 
 template <bool BF16, int D, bool TURN, bool READ>
-__global__ __launch_bounds__(256) void paged_rows_kernel(PagedPools c, Q8Seqs q, int n_layers, int n, int64_t tokens, Q8Rows kr, Q8Rows vr,
+__global__ __launch_bounds__(256) void paged_rows_kernel(PagedPools c, Q8Seqs q, int n_layers, int n, uint32_t tokens, Q8Rows kr, Q8Rows vr,
                                                          Rotation rot, unsigned int* __restrict__ dropped) {
     using X = Piece<BF16>;
     constexpr int ES = BF16 ? 2 : 4;
     constexpr int TPT = D / 2 / X::N;  // threads on a token
-    const int64_t t = (int64_t)blockIdx.x * (256 / TPT) + threadIdx.x / TPT;
+    const uint32_t t = blockIdx.x * (256 / TPT) + threadIdx.x / TPT;
     if (t >= tokens) return;
     const int p = threadIdx.x % TPT * X::N;  // the first of this thread's pairs
     const Token x = token_of(q, n, t, c.n_pages, c.page, rot);
@@ -135,11 +135,11 @@ __global__ __launch_bounds__(256) void paged_rows_kernel(PagedPools c, Q8Seqs q,
 template <bool READ>
 hipError_t launch_rows_of(Elem e, const PagedPools& c, const Q8Seqs& q, int n_layers, int n, const Q8Rows& k, const Q8Rows& v,
                           const Rotation& rot, unsigned int* dropped, hipStream_t s) {
-    const int64_t tokens = (int64_t)q.B * n;
-    const int per_block = 256 / (c.d / 2 / (e == Elem::BF16 ? 8 : 4));
-    const int64_t bx = (tokens + per_block - 1) / per_block;
+    const uint32_t tokens = (uint32_t)q.B * (uint32_t)n;  // at most 2^27
+    const uint32_t per_block = 256 / (c.d / 2 / (e == Elem::BF16 ? 8 : 4));
+    const uint32_t bx = (tokens + per_block - 1) / per_block;
     const int64_t by = std::min<int64_t>(2 * (int64_t)n_layers * c.H, 65534);  // keys and values of a slab side by side
-    const dim3 grid((unsigned)bx, (unsigned)by);
+    const dim3 grid(bx, (unsigned)by);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, c, q, n_layers, n, tokens, k, v, rot, dropped); };
     const bool turn = rot.tab != nullptr;
     if (e == Elem::BF16) {
