@@ -23,7 +23,7 @@
 //
 // What bounds it: bytes, where there are enough of them.  Keys and values are read once, past the caches and by whole lines of
 // 128 bytes, a tile's 16 KB at a time by each of 8 waves a CU: 64 sequences of 8,192 tokens, 8 KV heads, 2.15 GB in 339 us, 6.35 TB/s
-// (loads alone in the same pattern 6.8; through the caches 5.3), of up to 16,384 in 333, one of 32,768 134 MB in 27 and 4 to
+// (loads alone in the same pattern 6.8; through the caches 5.3), of up to 16,384 in 331, one of 32,768 134 MB in 27 and 4 to
 // join (loads alone 23).  Asking for a tile's keys while the one before is multiplied was no faster, with registers for two
 // tiles or with the keys' alone.  Below some thousand tokens a sequence it is the way through one step: lengths, pages, keys, the tile's
 // products and the joining of the waves one after the other, 7.2 us for 130 tokens.  Pieces are joined by a second kernel: by the last
