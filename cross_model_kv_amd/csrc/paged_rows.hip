@@ -5,7 +5,6 @@
 // rounded once; values, and keys without a table, are moved as they are.
 //
 // A thread owns 16 bytes of a token's low half and the 16 bytes of the high half that pair with them, in one layer and head, of
-// A thread owns 16 bytes of a token's low half and the 16 bytes of the high half that pair with them, in one layer and head, of
 // keys or of values: nothing crosses lanes.  Every element moves once, past the caches.  Bytes bound it: 8,192 bf16 tokens
 // of 64 layers and 8 heads enter in 721 us, 6.0 TB/s (a copy of 4 GiB: 4.7; through the caches and with keys and values in
 // one thread, four slabs at a time, 883), 4,096 of 40 layers are read back stripped in 223, 6.0 TB/s (265).  One decode step's
