@@ -41,6 +41,7 @@
 namespace kvmap {
 namespace {
 
+constexpr int kWaves = 4;
 constexpr int kTile = kQ8Step / kWaves;  // tokens of a wave's step
 
 // One tile's codes as loaded: keys of 4 x 16 tokens, values of D dims, and the lane's scales (the
@@ -65,6 +66,23 @@ using RowWeights = PartWeights<BF16 ? 2 : 3>;
 __host__ __device__ constexpr int per_cu(bool bf16, int nt) { return bf16 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 2 : 1); }
 template <bool BF16, int NT>
 constexpr bool kThird = per_cu(BF16, NT) == 3;
+
+// One row and 4 dims of the waves' sums, joined.
+template <int ROWS, int LDO>
+__device__ __forceinline__ void join_waves(const float (&s_o)[kWaves][ROWS][LDO], const float (&s_ml)[kWaves][ROWS][2], int row, int d4,
+                                           float& top, float& lsum, f32x4_t& sum) {
+    top = s_ml[0][row][0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, s_ml[w][row][0]);
+    sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    lsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(s_ml[w][row][0] - top);
+        sum += f * *(const f32x4_t*)&s_o[w][row][d4];
+        lsum = fmaf(f, s_ml[w][row][1], lsum);
+    }
+}
 
 // Steps of one item of each of 64 sequences, summed up to and including the lane's (at most 64 * 2^22).
 __device__ __forceinline__ uint32_t steps_upto(const Q8Attend& a, int b0, int end, int lane) {

@@ -231,25 +231,6 @@ __device__ __forceinline__ int settle_sum(double l, float& m, float& lf) {
     return -e;
 }
 
-constexpr int kWaves = 4;  // of the decode kernels' workgroups
-
-// One row and 4 dims of the waves' sums, joined.
-template <int ROWS, int LDO>
-__device__ __forceinline__ void join_waves(const float (&s_o)[kWaves][ROWS][LDO], const float (&s_ml)[kWaves][ROWS][2], int row, int d4,
-                                           float& top, float& lsum, f32x4_t& sum) {
-    top = s_ml[0][row][0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, s_ml[w][row][0]);
-    sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    lsum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(s_ml[w][row][0] - top);
-        sum += f * *(const f32x4_t*)&s_o[w][row][d4];
-        lsum = fmaf(f, s_ml[w][row][1], lsum);
-    }
-}
-
 // The query of a row.
 __device__ __forceinline__ int q8_query(const Q8Attend& a, int r) { return q8_divide(r, a.g_mul, a.g_shift); }
 
