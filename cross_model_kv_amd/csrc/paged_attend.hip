@@ -46,17 +46,14 @@ constexpr int kTile = 32;  // tokens of a wave's step
 
 // A row's queries as operands of S^T.  load() asks for what ready() makes them of; low: the lane's place in shared memory for
 // the second and third parts of turned bf16 queries (N rows tiles side by side), which all waves share.
-template <bool BF16, int D, bool TURN>
+template <bool BF16, int D, bool TURN, bool OWN>
 struct Queries;
 
-// From this many row tiles on, the low parts of turned queries are in shared memory.
-constexpr int kShared = 2;
-
-template <int D, bool TURN>
-struct Queries<true, D, TURN> {
+template <int D, bool TURN, bool OWN>
+struct Queries<true, D, TURN, OWN> {
     static constexpr int STEPS = D / 32;  // step s contracts dims 32 s + 8 g .. + 8
     bf16x8_t p[STEPS];
-    u32x4_t own[2 * STEPS];
+    u32x4_t own[TURN && OWN ? 2 * STEPS : 1];
     f32x4_t t[TURN ? STEPS * 2 : 1];
     // row: the query's first element; tab: its position's cosines and sines
     __device__ __forceinline__ void load(const void* row, int g, const float2* tab) {
@@ -87,7 +84,7 @@ struct Queries<true, D, TURN> {
             hi.set(b);
             p[s] = lo.p[0];
             p[s + STEPS / 2] = hi.p[0];
-            if (N < kShared)
+            if (OWN)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     own[k * STEPS + s] = __builtin_bit_cast(u32x4_t, lo.p[1 + k]);
@@ -109,7 +106,7 @@ struct Queries<true, D, TURN> {
         if (TURN)
 #pragma unroll
             for (int part = 1; part >= 0; --part) {
-                const bf16x8_t y = __builtin_bit_cast(bf16x8_t, N < kShared ? own[part * STEPS + st] : low[(part * STEPS + st) * N * 64]);
+                const bf16x8_t y = __builtin_bit_cast(bf16x8_t, OWN ? own[part * STEPS + st] : low[(part * STEPS + st) * N * 64]);
                 s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x0, y, s0, 0, 0, 0);
                 s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x1, y, s1, 0, 0, 0);
             }
@@ -118,8 +115,8 @@ struct Queries<true, D, TURN> {
     }
 };
 
-template <int D, bool TURN>
-struct Queries<false, D, TURN> {
+template <int D, bool TURN, bool OWN>
+struct Queries<false, D, TURN, OWN> {
     static constexpr int STEPS = D / 16;  // step s contracts dims 16 s + 4 g .. + 4
     f32x4_t p[STEPS];
     f32x4_t t[TURN ? STEPS : 1];
@@ -351,8 +348,9 @@ __host__ __device__ constexpr int per_simd(bool bf16, int d, int nt) {
     if (d == 64) return nt == 2 ? 2 : 4;
     return nt == 2 && !bf16 ? 1 : 2;
 }
-// Waves of a workgroup.  With two row tiles all of a CU's: the low parts of the queries then lie in its shared memory once.
-__host__ __device__ constexpr int waves_of(bool bf16, int d, int nt) { return nt == 2 && per_simd(bf16, d, nt) > 1 ? 8 : 4; }
+// Waves of a workgroup.  (8 in one workgroup a CU, with two row tiles: 22.3 us for 23.4 on 4 drafted tokens of 16 sequences of up to 5,003, 4
+// heads of 64 dims, but 26.5 for 20.5 on 9 of 20 of up to 900, and 161 for 132 on 16 of 16 of up to 8,192, 8 heads of 128 dims, G 8.)
+constexpr int kGroup = 4;
 
 // Steps of one item of each of 64 sequences, summed up to and including the lane's.
 __device__ __forceinline__ uint32_t steps_upto(const Q8Attend& a, int b0, int step, int lane) {
@@ -376,17 +374,18 @@ __device__ __forceinline__ void join_own(const float (*o)[ROWS][LDO], const floa
     }
 }
 
-template <bool BF16, int D, int NT, bool TURN, bool STREAM, int W>
-__global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT))) void paged_decode_kernel(Q8Attend a, Rotation rot, Q8Pieces sp) {
-    constexpr int ROWS = 16 * NT, ES = BF16 ? 2 : 4, LDO = D + 4, THREADS = 64 * W, STEP = kTile * W;
-    constexpr bool SHARES = BF16 && TURN && NT >= kShared;
+template <bool BF16, int D, int NT, bool TURN, bool STREAM>
+__global__ __launch_bounds__(64 * kGroup, (per_simd(BF16, D, NT))) void paged_decode_kernel(Q8Attend a, Rotation rot, Q8Pieces sp) {
+    constexpr int W = kGroup, ROWS = 16 * NT, ES = BF16 ? 2 : 4, LDO = D + 4, THREADS = 64 * W, STEP = kTile * W;
+    constexpr bool SHARES = BF16 && TURN && NT > 1;
     constexpr int LOW = SHARES ? 2 * (D / 32) * NT * 64 : 1;
-    typedef Queries<BF16, D, TURN> Q;
+    typedef Queries<BF16, D, TURN, !SHARES> Q;
     typedef Values<BF16, D> V;
     typedef RowWeights<BF16> Weights;
-    __shared__ float s_o[W][ROWS][LDO];
+    static_assert(LOW * sizeof(u32x4_t) <= W * ROWS * LDO * sizeof(float), "the queries' parts lie where the sums come later");
+    __shared__ __attribute__((aligned(16))) float s_o[W][ROWS][LDO];
     __shared__ float s_ml[W][ROWS][2];
-    __shared__ u32x4_t s_low[LOW];
+    u32x4_t* const s_low = (u32x4_t*)&s_o[0][0][0];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int H = a.c.H, G = a.Hq / H, R = a.n_q * G;
     const int P = a.c.page, logP = 31 - __clz(P);
@@ -483,15 +482,16 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT))) void paged_decode_
         Q q[NT];
         int end[NT];
         const int first_end = len - a.n_q + 1;  // the fewest tokens that a row sees
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        auto load_query = [&](auto& to, int n) {
             const int r = min(rb * ROWS + n * 16 + c, R - 1);  // (rows past the last are not stored)
             const int i = q8_query(a, r), hq = h * G + r - i * G;
             end[n] = first_end + i;
             const int pos = bad ? 0 : max(end[n] - 1, 0);
-            q[n].load((const char*)a.q.base + ((int64_t)b * a.q.seq + (int64_t)hq * a.q.head + (int64_t)i * a.q.token) * ES, g,
-                      TURN ? rot.tab + (int64_t)pos * (D / 2) : nullptr);
-        }
+            to.load((const char*)a.q.base + ((int64_t)b * a.q.seq + (int64_t)hq * a.q.head + (int64_t)i * a.q.token) * ES, g,
+                    TURN ? rot.tab + (int64_t)pos * (D / 2) : nullptr);
+        };
+#pragma unroll
+        for (int n = 0; n < NT; ++n) load_query(q[n], n);
         // A tile's keys and values.  A lane's 8 tokens of values lie in one page, which has whole 16 tokens, and so do the rows of
         // keys of one load.  What one workgroup alone reads is read past the caches (STREAM).
         Keys<BF16, D> k;
@@ -523,7 +523,7 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT))) void paged_decode_
             for (int t = 0; t < D / 16; ++t) o[n][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
         // A tile's scores y of the lane's tokens tok .. tok + 8.
-        auto scores = [&](int t0, int p0, int p1, float (&y)[NT][8]) {
+        auto scores = [&](const auto& q, int t0, int p0, int p1, float (&y)[NT][8]) {
             const int tok = t0 + 8 * g;
             if (SHARES) asm volatile("" : "+v"(low));  // keeps the low parts where they are: registers are full
             f32x4_t s[2][NT];
@@ -562,7 +562,7 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT))) void paged_decode_
             float y[NT][8], top[NT];
             load_keys(t0, p0, p1);
             v.template load<STREAM>(values_at(t0, p0, p1), D * ES);
-            scores(t0, p0, p1, y);
+            scores(q, t0, p0, p1, y);
             bool move = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -611,6 +611,7 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT))) void paged_decode_
             p0 = n0, p1 = n1;
             if (tile + 2 * W < t_end) n0 = page_of(tile + 2 * W, 0), n1 = page_of(tile + 2 * W, 1);
         }
+        if (SHARES) __syncthreads();  // the parts of the queries have been read
         // join the waves: a fixed order, so the result does not depend on who is first
         asm volatile("" : "+v"(tid));  // (nor across the loop above)
         const int row0 = tid & 15, dim0 = (tid & 63) >> 4 << 4;
@@ -636,7 +637,14 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT))) void paged_decode_
                 }
         }
         if (apart) {
-            // The tiles left out above, query by query, each with what it sees, onto the wave's sums where they are now.
+            // The tiles left out above, query by query, each with what it sees, onto the wave's sums where they are now.  (The
+            // queries once more: registers are free, and their parts are overwritten.)
+            Queries<BF16, D, TURN, true> again[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                load_query(again[n], n);
+                again[n].template ready<NT>(nullptr, false);
+            }
             for (int t1 = t_begin + wave; t1 < t_end; t1 += W) {
                 const int t0 = t1 * kTile, tok = t0 + 8 * g;
                 if (t0 + kTile <= first_end) continue;
@@ -646,7 +654,7 @@ __global__ __launch_bounds__(64 * W, (per_simd(BF16, D, NT))) void paged_decode_
                 if (!__any(odd(v, first_end - tok, len - tok))) continue;
                 load_keys(t0, p0, p1);
                 float y[NT][8];
-                scores(t0, p0, p1, y);
+                scores(again, t0, p0, p1, y);
                 Weights w[NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -710,8 +718,7 @@ Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_l
     p.rows = 16 * nt;
     p.row_blocks = (int)((R + p.rows - 1) / p.rows);
     const double items = (double)B * H * p.row_blocks;
-    const int waves = waves_of(bf16, d, nt);
-    const int steps = steps_of(max_len, max_len, kTile * waves), held = 4 * per_simd(bf16, d, nt) / waves * cus;
+    const int steps = steps_of(max_len, max_len, kTile * kGroup), held = 4 * per_simd(bf16, d, nt) / kGroup * cus;
     p.splits = max_len > (items < cus ? kWhole : items < held ? kFull : kMany) && held / p.row_blocks > 1;
     // cut: a workgroup for every step that the lengths can bring, up to what the chip holds at once; else one for every item
     p.grid = p.splits ? (int)std::min<double>(held / p.row_blocks, (double)B * H * steps) * p.row_blocks : (int)items;
@@ -720,14 +727,13 @@ Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_l
 
 template <bool BF16, int D, int NT, bool TURN>
 static hipError_t launch_decode(const Q8Attend& a, const Rotation& rot, const Q8Pieces& sp, const Q8Plan& p, hipStream_t s) {
-    constexpr int W = waves_of(BF16, D, NT);
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)p.grid), dim3(64 * W), 0, s, a, rot, sp); };
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)p.grid), dim3(64 * kGroup), 0, s, a, rot, sp); };
     if constexpr (NT == 2)
         if (p.row_blocks > 1) {
-            go(paged_decode_kernel<BF16, D, NT, TURN, false, W>);
+            go(paged_decode_kernel<BF16, D, NT, TURN, false>);
             return hipGetLastError();
         }
-    go(paged_decode_kernel<BF16, D, NT, TURN, true, W>);
+    go(paged_decode_kernel<BF16, D, NT, TURN, true>);
     return hipGetLastError();
 }
 
