@@ -24,8 +24,8 @@
 // What bounds it: bytes, where there are enough of them.  Keys and values are read once, past the caches and by whole lines of
 // 128 bytes, a tile's 16 KB at a time by each of 8 waves a CU: 64 sequences of 8,192 tokens, 8 KV heads, 2.15 GB in 339 us, 6.35 TB/s
 // (loads alone in the same pattern 6.8; through the caches 5.3), of up to 16,384 in 331, one of 32,768 134 MB in 27 and 4 to
-// join (loads alone 23).  Asking for a tile's keys while the one before is multiplied was no faster, with registers for two
-// tiles or with the keys' alone.  Below some thousand tokens a sequence it is the way through one step: lengths, pages, keys, the tile's
+// join (loads alone 23).  Asking for a tile's keys and values while the one before is multiplied was slower, 61 us for 56 on
+// 8 sequences of 8,192.  Below some thousand tokens a sequence it is the way through one step: lengths, pages, keys, the tile's
 // products and the joining of the waves one after the other, 7.2 us for 130 tokens.  Pieces are joined by a second kernel: by the last
 // piece to come, through memory past the caches, it took 58 us for 38 on one sequence of 32,768 tokens and 63 for 61 on 8 of 8,192.
 
@@ -45,7 +45,7 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 constexpr int kTile = 32;  // tokens of a wave's step
 
 // A row's queries as operands of S^T.  load() asks for what ready() makes them of; low: the lane's place in shared memory for
-// the second and third parts of turned bf16 queries (N rows tiles side by side), which all waves share.
+// the second and third parts of turned bf16 queries (N row tiles side by side), which all waves share; OWN: they are in registers.
 template <bool BF16, int D, bool TURN, bool OWN>
 struct Queries;
 
