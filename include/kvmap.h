@@ -645,7 +645,7 @@ int kvmap_paged_dropped(kvmap_ctx* ctx, uint32_t* n, void* stream);
  * touch it, whatever they hold; infinities and NaN in those that it sees reach it as the formula has it (with `rot`, a key
  * that is not finite makes every row that sees it NaN).
  * q, out, pages, max_pages, len, max_len, lse, and what is out of range: as in kvmap_q8_attend, with rows of the cache's dtype.
- * bf16: products on the matrix cores with bf16 operands, softmax weights with 16 bits and queries that were rotated with 24.  fp32:
+ * bf16: products on the matrix cores with bf16 operands, softmax weights and queries that were rotated with 24 bits.  fp32:
  * products of fp32 operands.  Products' sums and statistics in fp32, the sum of a row's weights in fp64.
  * Repeated calls give identical outputs.  (Where a long cache is cut follows the lengths of all sequences, so a sequence's
  * rounding may differ between calls with different company.)  Asynchronous on `stream`.  Long caches are split over
