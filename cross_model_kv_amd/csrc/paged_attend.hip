@@ -44,6 +44,35 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 32;  // tokens of a wave's step
 
+// The upper 16 bits of two fp32 numbers side by side: the first bf16 parts that their remainders follow.
+__device__ __forceinline__ uint32_t upper_halves(float x0, float x1) {
+    return __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
+}
+// What x >= 0 has beyond its upper 16 bits: not negative, and not zero where x is not (at least 2^-126 of it).
+__device__ __forceinline__ float beyond_half(float x) {
+    return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u), fminf(x, 0x1p-126f));
+}
+
+// A turned query's 8 elements as three parts of 8 bits, each cut off, so that they hold all 24 bits (and 2^-125 more at most), all have
+// the element's sign, and none is zero where the element is not: then a key's infinity times the element is the same one in
+// every part's product, and the score has it.
+struct SplitQuery {
+    u32x4_t p[3];
+    __device__ __forceinline__ void set(const float* x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float r0 = fabsf(x[2 * i]), r1 = fabsf(x[2 * i + 1]);
+            const uint32_t signs = upper_halves(x[2 * i], x[2 * i + 1]) & 0x80008000u;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                p[k][i] = upper_halves(r0, r1) | signs;
+                r0 = beyond_half(r0);
+                r1 = beyond_half(r1);
+            }
+        }
+    }
+};
+
 // A row's queries as operands of S^T.  load() asks for what ready() makes them of; low: the lane's place in shared memory for
 // the second and third parts of turned bf16 queries (N row tiles side by side), which all waves share; OWN: they are in registers.
 template <bool BF16, int D, bool TURN, bool OWN>
@@ -79,22 +108,22 @@ struct Queries<true, D, TURN, OWN> {
                 a[e] = fmaf(-y, sn, x * cs);
                 b[e] = fmaf(x, sn, y * cs);
             }
-            Parts<3> lo, hi;
+            SplitQuery lo, hi;
             lo.set(a);
             hi.set(b);
-            p[s] = lo.p[0];
-            p[s + STEPS / 2] = hi.p[0];
+            p[s] = __builtin_bit_cast(bf16x8_t, lo.p[0]);
+            p[s + STEPS / 2] = __builtin_bit_cast(bf16x8_t, hi.p[0]);
             if (OWN)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    own[k * STEPS + s] = __builtin_bit_cast(u32x4_t, lo.p[1 + k]);
-                    own[k * STEPS + s + STEPS / 2] = __builtin_bit_cast(u32x4_t, hi.p[1 + k]);
+                    own[k * STEPS + s] = lo.p[1 + k];
+                    own[k * STEPS + s + STEPS / 2] = hi.p[1 + k];
                 }
             else if (write)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    low[(k * STEPS + s) * N * 64] = __builtin_bit_cast(u32x4_t, lo.p[1 + k]);
-                    low[(k * STEPS + s + STEPS / 2) * N * 64] = __builtin_bit_cast(u32x4_t, hi.p[1 + k]);
+                    low[(k * STEPS + s) * N * 64] = lo.p[1 + k];
+                    low[(k * STEPS + s + STEPS / 2) * N * 64] = hi.p[1 + k];
                 }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -206,15 +235,6 @@ struct Keys<false, D> {
     }
     __device__ __forceinline__ u32x4_t step(int mt, int st) const { return k[mt][st]; }
 };
-
-// The upper 16 bits of two fp32 numbers side by side: the first bf16 parts that their remainders follow.
-__device__ __forceinline__ uint32_t upper_halves(float x0, float x1) {
-    return __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
-}
-// What x >= 0 has beyond its upper 16 bits: not negative, and not zero where x is not (at least 2^-126 of it).
-__device__ __forceinline__ float beyond_half(float x) {
-    return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u), fminf(x, 0x1p-126f));
-}
 
 // The weights of a lane's 8 tokens.  In bf16 as three parts of 8 bits, each cut off, so that they hold all that fp32 does, none is
 // negative, and none is zero where the weight is not: then an infinity that a row sees is one in its sum, and no 0 times it.

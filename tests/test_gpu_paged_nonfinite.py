@@ -1,0 +1,65 @@
+"""Attention over the paged cache with infinities and NaN in keys and values, with and without rotated queries: by whole sequences
+and by pieces, with one tile of rows, with two, and with two blocks of them.  What is finite is held to test_gpu_paged.py's tolerances."""
+
+import numpy as np
+import pytest
+
+from oracle import paged_oracle as O
+from test_gpu_paged import THETA, _attend_close, _dev, _f64, _ints, _table
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+ODD = [np.inf, -np.inf, np.nan]
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    from cross_model_kv_amd import kvmap as K
+    c = K.Context(0)
+    yield c
+    c.close()
+
+
+def _case(rng, lens, H, d, page):
+    """A pool, its tables, and how to reach a sequence's token in it."""
+    need = [-(-l // page) for l in lens]
+    pages = _table(rng, sum(need) + 2, need, 5000 // page + 1)
+    k, v = rng.standard_normal((2, 1, sum(need) + 2, H, page, d))
+    return k, v, pages, lambda x, b, h, pos: x[0, pages[b][pos // page], h, pos % page]
+
+
+def _run(ctx, k, v, q, pages, lens, dtype, d, rope, cut, scale=None):
+    """What the call gives, the oracle's answer, and the oracle's with every key element finite (whose sums of |q k| bound scores)."""
+    from cross_model_kv_amd import kvmap as K
+    (kt, k64), (vt, v64), (qt, q64) = _dev(k, dtype), _dev(v, dtype), _dev(q, dtype)
+    max_len = 5000 if cut else max(lens)
+    rot = ctx.rope_table(max_len, d, theta=THETA) if rope else None
+    r64 = None if rot is None else _f64(rot)[:max(lens)]
+    out, lse = ctx.paged_attend(K.PagedCache(kt, vt), qt, _ints(pages), _ints(lens), max_len, rope=rot, lse=True, scale=scale)
+    torch.cuda.synchronize()
+    scale = d ** -0.5 if scale is None else scale
+    ref = O.attend(dict(k=k64, v=v64), q64, pages, lens, scale, rot=r64)
+    tame = O.attend(dict(k=np.where(np.isfinite(k64), k64, 0), v=v64), q64, pages, lens, scale, rot=r64)
+    return _f64(out), _f64(lse), ref, tame
+
+
+@pytest.mark.parametrize("cut", [False, True], ids=["own", "pieces"])
+@pytest.mark.parametrize("rope", [False, True], ids=["plain", "turned"])
+@pytest.mark.parametrize("n_q,G", [(1, 3), (4, 6), (16, 3)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 128), ("f32", 64)])
+def test_keys(ctx, dtype, d, n_q, G, rope, cut):
+    """A key with an element that is not finite, early in a sequence or among the last tokens that only some rows see.  An infinity
+    gives a score of -infinity, which has no weight, or of +infinity, by the sign of the query's element: rows of both kinds."""
+    lens, H, page = [40, 300, 640, 33, 700], 2, 16
+    rng = np.random.default_rng([1, d, n_q, G])
+    k, v, pages, at = _case(rng, lens, H, d, page)
+    for b, l in enumerate(lens):
+        for h in range(H):
+            at(k, b, h, 5 if b % 2 else l - 1 - n_q // 2)[rng.integers(d)] = ODD[2] if b == 4 else ODD[(b + h) % 2]
+    q = 1.5 * rng.standard_normal((len(lens), n_q, H * G, d))
+    out, lse, ref, tame = _run(ctx, k, v, q, pages, lens, dtype, d, rope, cut)
+    finite = np.isfinite(ref[0][:4]).all(-1)
+    assert finite.any() and not finite.all()
+    _attend_close(out, lse, (ref[0], ref[1], ref[2], tame[3]), dtype, d, lens, rope)
