@@ -63,3 +63,31 @@ def test_keys(ctx, dtype, d, n_q, G, rope, cut):
     finite = np.isfinite(ref[0][:4]).all(-1)
     assert finite.any() and not finite.all()
     _attend_close(out, lse, (ref[0], ref[1], ref[2], tame[3]), dtype, d, lens, rope)
+
+
+@pytest.mark.parametrize("cut", [False, True], ids=["own", "pieces"])
+@pytest.mark.parametrize("rope", [False, True], ids=["plain", "turned"])
+@pytest.mark.parametrize("n_q,G", [(5, 3), (8, 4), (16, 3), (16, 5)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 128), ("f32", 64)])
+def test_values_that_later_rows_alone_see(ctx, dtype, d, n_q, G, rope, cut):
+    """Drafted tokens with infinities and NaN in some dims of their values, and both in keys and values past a sequence's end: the rows
+    that see a value have it, by its weight's sum, and no other row does.  (Such tiles are multiplied after the others, row by row, with
+    the queries turned once more.)"""
+    lens, H, page = [n_q, 100, 640, 33, 1], 2, 16
+    rng = np.random.default_rng([2, d, n_q, G])
+    k, v, pages, at = _case(rng, lens, H, d, page)
+    used = sum((p[:-(-l // page)] for p, l in zip(pages, lens)), [])
+    for x in (k, v):
+        x[:, [i for i in range(x.shape[1]) if i not in used]] = np.nan
+        for b, l in enumerate(lens):
+            for pos in range(l, -(-l // page) * page):
+                for h in range(H):
+                    at(x, b, h, pos)[:] = ODD[pos % 3]
+    for b, l in enumerate(lens[:4]):
+        for h in range(H):
+            for j in range(1 + h, min(n_q, l), 2):       # of tokens l - 1 - j, the last j + 1 rows see it
+                at(v, b, h, l - 1 - j)[rng.choice(d, 6, replace=False)] = [np.nan, np.inf, -np.inf, np.inf, np.inf, -np.inf]
+    q = 1.5 * rng.standard_normal((len(lens), n_q, H * G, d))
+    out, lse, ref, tame = _run(ctx, k, v, q, pages, lens, dtype, d, rope, cut)
+    fine = _attend_close(out, lse, ref, dtype, d, lens, rope)
+    assert not fine[:4, -1].all() and fine[4].all() and not np.isnan(ref[1]).any()
