@@ -238,6 +238,9 @@ struct Keys<false, D> {
 
 // The weights of a lane's 8 tokens.  In bf16 as three parts of 8 bits, each cut off, so that they hold all that fp32 does, none is
 // negative, and none is zero where the weight is not: then an infinity that a row sees is one in its sum, and no 0 times it.
+// (Where the weight is not zero itself, nor a factor that it meets later, as m grows and in the joins: each is a power of 2 by m's
+// difference to a larger m.  A score is never more than kSlack over its m, and the largest m at most 1 over lse, in base 2: weights of
+// 2^-110 of the row's sum and more stay.)
 // (Two parts, 16 bits: where a row's values nearly cancel, outputs were up to 490 steps of bf16 off, for 21 now and 102 of the
 // formula in 32-bit torch calls, on 64 sequences of up to 16,384 tokens.  The third costs nothing on long sequences and 2 to 4 % on
 // short ones: 4 drafted tokens of 64 sequences of up to 900, 37.4 us for 38.8.)

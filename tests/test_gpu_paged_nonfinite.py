@@ -91,3 +91,39 @@ def test_values_that_later_rows_alone_see(ctx, dtype, d, n_q, G, rope, cut):
     out, lse, ref, tame = _run(ctx, k, v, q, pages, lens, dtype, d, rope, cut)
     fine = _attend_close(out, lse, ref, dtype, d, lens, rope)
     assert not fine[:4, -1].all() and fine[4].all() and not np.isnan(ref[1]).any()
+
+
+@pytest.mark.parametrize("order", ["same tile", "other wave", "later step", "other piece", "before"])
+@pytest.mark.parametrize("rope", [False, True], ids=["plain", "turned"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_infinity_far_below_the_largest_score(ctx, dtype, rope, order):
+    """An infinite value whose score is 69 nats under the row's largest (a weight of 2^-99.5) stays one, wherever the two tokens lie;
+    150 nats under, it is that or NaN, and nothing but its dim is touched."""
+    from cross_model_kv_amd import kvmap as K
+    d, page, T = 128, 16, 4600
+    odd, high = {"same tile": (3, 20), "other wave": (3, 40), "later step": (3, 700), "other piece": (3, 4500), "before": (700, 3)}[order]
+    rng = np.random.default_rng(3)
+    for nats in (69.0, 150.0):
+        k, v = np.zeros((1, T // page + 1, 1, page, d)), rng.standard_normal((1, T // page + 1, 1, page, d))
+        k[0, high // page, 0, high % page, 0] = nats / 8
+        v[0, odd // page, 0, odd % page, 7], v[0, odd // page, 0, odd % page, 9] = np.inf, -np.inf
+        q = np.zeros((1, 1, 3, d))
+        q[..., 0] = 8.0
+        (kt, _), (vt, v64), (qt, _) = _dev(k, dtype), _dev(v, dtype), _dev(q, dtype)
+        rot = None
+        if rope:                                         # turns by nothing
+            rot = torch.zeros((T, d // 2, 2), device="cuda")
+            rot[..., 0] = 1.0
+        out, lse = ctx.paged_attend(K.PagedCache(kt, vt), qt, _ints([list(range(T // page + 1))]), _ints([T]), T, scale=1.0, rope=rot,
+                                    lse=True)
+        torch.cuda.synchronize()
+        out, lse = _f64(out), _f64(lse)
+        seen = v64[0, high // page, 0, high % page]
+        rest = [i for i in range(d) if i not in (7, 9)]
+        # the other 4,599 tokens weigh e^-69 each; fp32's roundings of a score of 69 and one of the answer
+        assert np.allclose(lse, nats, rtol=4 * 2.0 ** -24)
+        assert (abs(out[..., rest] - seen[rest]) <= (2.0 ** -8 if dtype == "bf16" else 4 * 2.0 ** -24) * abs(seen[rest])).all()
+        if nats < 76:
+            assert (out[..., 7] == np.inf).all() and (out[..., 9] == -np.inf).all()
+        else:
+            assert not np.isfinite(out[..., [7, 9]]).any() and not (out[..., 7] == -np.inf).any() and not (out[..., 9] == np.inf).any()
