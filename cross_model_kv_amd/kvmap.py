@@ -756,7 +756,8 @@ class Context:
     def paged_read(self, cache: PagedCache, pages, start, n: int, count=None, layer: int = 0, n_layers: int | None = None,
                    rope=None, out_k=None, out_v=None, stream=None):
         """kvmap_paged_read: (k, v) [n_layers][B][H][n][d], the n tokens from start[b] of every sequence, zeros past count[b];
-        with a table (rope_table) the keys stripped of their rotation.  n_layers defaults to the layers from `layer`
+        with a table (rope_table) the keys stripped of their rotation (one that scales by s, too, takes a table of cosines and
+        sines over s * s for that).  n_layers defaults to the layers from `layer`
         on.  What the call allocates belongs to `stream`."""
         torch = _torch()
         L = cache.L - layer if n_layers is None else n_layers

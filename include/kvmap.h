@@ -610,7 +610,8 @@ typedef struct {
 } kvmap_rotation;
 
 /* table[p][i] = (cos a, sin a), a = (rope->pos0 + p) f_i with the frequencies of `rope`, formed in float64.  A caller that
- * scales its rotations, or whose positions do not run evenly, fills a table of its own.  Asynchronous on `stream`, allocates
+ * scales its rotations, or whose positions do not run evenly, fills a table of its own (but a table that scales, cos^2 + sin^2
+ * = n other than 1, strips nothing: kvmap_paged_read takes one of (cos / n, sin / n) for that).  Asynchronous on `stream`, allocates
  * nothing.  Errors: SHAPE (n_pos outside 1 .. 2^26), UNSUPPORTED (head_dim, style), INVALID_ARGUMENT. */
 int kvmap_rope_table(kvmap_ctx* ctx, const kvmap_rope* rope, int64_t n_pos, int32_t head_dim, float* table, void* stream);
 
@@ -627,8 +628,9 @@ int kvmap_paged_append(kvmap_ctx* ctx, const kvmap_paged_cache* cache, int32_t l
                        const kvmap_q8_seqs* seqs, int32_t n, const kvmap_q8_rows* k, const kvmap_q8_rows* v,
                        const kvmap_rotation* rot, void* stream);
 /* Read the same tokens: k, v rows (layer - layer0, b, head, i) get them, keys turned by the opposite angles where `rot` is
- * given (stripped); zeros for count[b] <= i < n, and NaN where an append would have left a token out.  Asynchronous on
- * `stream`, allocates nothing, may be captured.  Errors as kvmap_paged_append. */
+ * given: pair (x, y) comes as (x cos + y sin, y cos - x sin), which strips what an append with a table of rotations has turned
+ * (with one that scales, see kvmap_rope_table); zeros for count[b] <= i < n, and NaN where an append would have left a token
+ * out.  Asynchronous on `stream`, allocates nothing, may be captured.  Errors as kvmap_paged_append. */
 int kvmap_paged_read(kvmap_ctx* ctx, const kvmap_paged_cache* cache, int32_t layer0, int32_t n_layers,
                      const kvmap_q8_seqs* seqs, int32_t n, const kvmap_q8_rows* k, const kvmap_q8_rows* v,
                      const kvmap_rotation* rot, void* stream);
