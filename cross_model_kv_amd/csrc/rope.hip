@@ -11,6 +11,8 @@
 // an fp32 product p * f_i is off by ~1e-3 rad at p = 32767, the size of deviation the
 // VeloxQuant-MLX "Metal kernel" section reports for its fp32 path.
 
+#include <algorithm>
+
 #include "common.h"
 #include "internal.h"
 
@@ -23,14 +25,14 @@ __device__ __forceinline__ double rope_freq(const RopeFreqs& fr, int i, int d) {
 __global__ __launch_bounds__(256) void rope_table_kernel(float2* __restrict__ tab, int64_t T, int d,
                                                          const RopeFreqs fr, int64_t pos0) {
     const int half = d / 2;
-    const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (idx >= T * half) return;
-    const int64_t t = idx / half;
-    const int i = (int)(idx - t * half);
-    const double a = (double)(pos0 + t) * rope_freq(fr, i, d);
-    double s, c;
-    sincos(a, &s, &c);
-    tab[idx] = make_float2((float)c, (float)s);
+    for (int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; idx < T * half; idx += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t t = idx / half;
+        const int i = (int)(idx - t * half);
+        const double a = (double)(pos0 + t) * rope_freq(fr, i, d);
+        double s, c;
+        sincos(a, &s, &c);
+        tab[idx] = make_float2((float)c, (float)s);
+    }
 }
 
 // Recode table: (cos A, sin A) with A = (pos0_s + t) f_s,i - (pos0_t + t) f_t,i, formed in
@@ -42,27 +44,30 @@ __global__ __launch_bounds__(256) void rope_diff_table_kernel(float2* __restrict
                                                               const RopeFreqs fs, int64_t pos0_s,
                                                               const RopeFreqs ft, int64_t pos0_t) {
     const int half = d / 2;
-    const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (idx >= T * half) return;
-    const int64_t t = idx / half;
-    const int i = (int)(idx - t * half);
-    const double a = (double)(pos0_s + t) * rope_freq(fs, i, d) - (double)(pos0_t + t) * rope_freq(ft, i, d);
-    double s, c;
-    sincos(a, &s, &c);
-    tab[idx] = make_float2((float)c, (float)s);
+    for (int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; idx < T * half; idx += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t t = idx / half;
+        const int i = (int)(idx - t * half);
+        const double a = (double)(pos0_s + t) * rope_freq(fs, i, d) - (double)(pos0_t + t) * rope_freq(ft, i, d);
+        double s, c;
+        sincos(a, &s, &c);
+        tab[idx] = make_float2((float)c, (float)s);
+    }
 }
+
+// Workgroups of 256 for a table of T positions: a launch takes fewer than 2^32 work-items in a dimension, longer tables go round.
+constexpr int64_t kTableBlocks = int64_t(1) << 23;
+static_assert(kTableBlocks * 256 < int64_t(1) << 32, "more work-items than a launch takes");
+static unsigned table_blocks(int64_t T, int d) { return (unsigned)std::min((T * (d / 2) + 255) / 256, kTableBlocks); }
 
 hipError_t launch_rope_diff_table(float2* tab, int64_t T, int d, const RopeFreqs& fs, int64_t pos0_s,
                                   const RopeFreqs& ft, int64_t pos0_t, hipStream_t s) {
-    const int64_t n = T * (d / 2);
-    const unsigned blocks = (unsigned)((n + 255) / 256);
+    const unsigned blocks = table_blocks(T, d);
     hipLaunchKernelGGL(rope_diff_table_kernel, dim3(blocks), dim3(256), 0, s, tab, T, d, fs, pos0_s, ft, pos0_t);
     return hipGetLastError();
 }
 
 hipError_t launch_rope_table(float2* tab, int64_t T, int d, const RopeFreqs& fr, int64_t pos0, hipStream_t s) {
-    const int64_t n = T * (d / 2);
-    const unsigned blocks = (unsigned)((n + 255) / 256);
+    const unsigned blocks = table_blocks(T, d);
     hipLaunchKernelGGL(rope_table_kernel, dim3(blocks), dim3(256), 0, s, tab, T, d, fr, pos0);
     return hipGetLastError();
 }

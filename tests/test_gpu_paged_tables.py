@@ -40,3 +40,18 @@ def test_stripping_scaled_rotations(ctx, dtype):
     tol = (2 * _u(dtype) * (1 + _u(dtype)) + 10 * 2.0 ** -24) * size
     assert (abs(_f64(once)[0, 0] - k64[0]) <= tol).all()
     assert (abs(_f64(twice)[0, 0] - k64[0] * scale ** 2) <= tol * scale ** 2).all()
+
+
+@pytest.mark.parametrize("n_pos,d", [(1 << 26, 128), ((1 << 26) - 3, 128), (1 << 26, 64)])
+def test_the_longest_tables(ctx, n_pos, d):
+    """Tables of 2^26 positions, more entries than a launch has work-items: every entry is written, and those at both ends and
+    between are float64's cosines and sines to half a step of fp32, 2^-25, and the float64 angle's own two roundings of up to 2^-27
+    each at 2^26."""
+    table = ctx.rope_table(n_pos, d, theta=1.0e4, out=torch.full((n_pos, d // 2, 2), 7.0, device="cuda"))
+    torch.cuda.synchronize()
+    for part in table.split(1 << 22):
+        assert bool((part.square().sum(-1) - 1).abs().le(1e-6).all())
+    for at in (0, 12345678, 1 << 25, n_pos - 200):
+        assert abs(_f64(table[at:at + 200]) - O.table(200, d, theta=1.0e4, pos0=at)).max() <= 2.0 ** -25 + 2 * 2.0 ** -27
+    del table, part
+    torch.cuda.empty_cache()
