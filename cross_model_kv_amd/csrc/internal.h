@@ -221,7 +221,7 @@ struct Q8Pieces {
 };
 Q8Pieces q8_pieces(const Q8Attend& a, const Q8Plan& p, void* scratch);
 size_t q8_piece_bytes(int grid, int rows, int d);
-size_t q8_scratch_bytes(int cus);  // enough for every plan
+size_t q8_scratch_bytes(int cus);  // enough for every plan of the 8-bit cache's attention
 Q8Plan q8_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus);
 // q8_prompt.hip's plan, or a plan with no rows where the call has too few of them.
 Q8Plan q8_prompt_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus);
@@ -236,7 +236,7 @@ struct Q8State {
     int cus = 0;
 };
 Q8State* q8_state(struct ::kvmap_ctx* c);
-// Allocates the scratch where there is none; `stream` is the call's, or NULL outside of one (q8_api.hip).
+// The scratch that both caches' attention shares, allocated where there is none; `stream` is the call's, or NULL outside of one (q8_api.hip).
 int ensure_scratch(Q8State* s, hipStream_t stream, bool in_call, const char* call);
 
 // ---- paged cache in the model's own type (paged_rows.hip, paged_attend.hip) -----------------------------
@@ -258,6 +258,7 @@ hipError_t launch_paged_read(Elem e, const PagedPools& c, const Q8Seqs& q, int n
 // a.c: k and v are one layer's pools, its scales are not used; work is dealt out, and pieces are joined through the scratch, as
 // the 8-bit cache's are.
 Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus);
+size_t paged_scratch_bytes(int cus);  // enough for every one of them
 hipError_t launch_paged_attend(Elem e, const Q8Attend& a, const Rotation& rot, const Q8Plan& p, void* scratch, hipStream_t s);
 
 // Error reporting shared by the C-ABI files: sets the calling thread's last-error string.

@@ -745,6 +745,18 @@ __global__ __launch_bounds__(64 * kGroup, (per_simd(BF16, D, NT))) void paged_de
 // that the chip holds (128 of 1,500: 133, cut 144; 64 of up to 1,400: 42 and 48; with 256 items for 512 places, fp32: 37 and 28).
 constexpr int kWhole = 256, kFull = 1024, kMany = 2048;
 
+// Workgroups that the chip holds at once.
+static int held_at_once(bool bf16, int d, int nt, int cus) { return 4 * per_simd(bf16, d, nt) / kGroup * cus; }
+
+// The most that a plan below leaves for the join: a piece of every workgroup that the chip holds.
+size_t paged_scratch_bytes(int cus) {
+    size_t most = 0;
+    for (bool bf16 : {false, true})
+        for (int d : {64, 128})
+            for (int nt : {1, 2}) most = std::max(most, q8_piece_bytes(held_at_once(bf16, d, nt, cus), 16 * nt, d));
+    return most;
+}
+
 Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_len, int cus) {
     Q8Plan p{};
     const bool bf16 = e == Elem::BF16;
@@ -753,7 +765,7 @@ Q8Plan paged_attend_plan(Elem e, int B, int n_q, int Hq, int H, int d, int max_l
     p.rows = 16 * nt;
     p.row_blocks = (int)((R + p.rows - 1) / p.rows);
     const double items = (double)B * H * p.row_blocks;
-    const int steps = steps_of(max_len, max_len, kTile * kGroup), held = 4 * per_simd(bf16, d, nt) / kGroup * cus;
+    const int steps = steps_of(max_len, max_len, kTile * kGroup), held = held_at_once(bf16, d, nt, cus);
     p.splits = max_len > (items < cus ? kWhole : items < held ? kFull : kMany) && held / p.row_blocks > 1;
     // cut: a workgroup for every step that the lengths can bring, up to what the chip holds at once; else one for every item
     p.grid = p.splits ? (int)std::min<double>(held / p.row_blocks, (double)B * H * steps) * p.row_blocks : (int)items;

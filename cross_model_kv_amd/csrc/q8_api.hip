@@ -3,6 +3,7 @@
 
 #include "../../include/kvmap.h"
 
+#include <algorithm>
 #include <cmath>
 
 #include "internal.h"
@@ -214,7 +215,7 @@ int kvmap::ensure_scratch(Q8State* s, hipStream_t stream, bool in_call, const ch
             return report(KVMAP_ERR_INVALID_ARGUMENT, "%s_attend: the stream is being captured and the context has no scratch "
                           "yet; call %s_reserve first", call, call);
     }
-    KVMAP_HIP(hipMalloc(&s->scratch, q8_scratch_bytes(s->cus)));
+    KVMAP_HIP(hipMalloc(&s->scratch, std::max(q8_scratch_bytes(s->cus), paged_scratch_bytes(s->cus))));
     return KVMAP_OK;
 }
 
