@@ -576,10 +576,15 @@ class Context:
 
     # A decode step makes these calls once a layer on a few rows, so their host time counts: no objects are made that
     # the call does not need, and the argument structs belong to the context (which one thread uses at a time).
+    def _own_ptr(self, t, name):
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} must be on the context's device")
+        return _dev_ptr(t, name)
+
     def _q8_ints(self, t, name, shape):
         if t.dtype is not _torch_module.int32 or t.shape != shape:
             raise ValueError(f"{name} must be int32 {list(shape)}")
-        return _dev_ptr(t, name)
+        return self._own_ptr(t, name)
 
     def _rows_args(self, cache, k, v, pages, start, n, count):
         """Fills the context's structs with a rows call's arguments; returns the number of layers."""
@@ -588,8 +593,8 @@ class Context:
         shape = (L, B, cache.H, n, cache.d)
         if k.shape != shape or v.shape != shape:
             raise ValueError(f"k and v must be {list(shape)} ([layers][B][H][n][d], or [B][H][n][d] of one layer)")
-        if not (k.is_cuda and v.is_cuda):
-            raise ValueError("k and v must be device tensors")
+        if not self.device == cache.index == k.get_device() == v.get_device():
+            raise ValueError("the cache, k and v must be on the context's device")
         seqs, rk, rv = self._seqs, self._rows[0], self._rows[1]
         rk.layer_stride, rk.seq_stride, rk.head_stride, rk.token_stride, k_last = k.stride()
         rv.layer_stride, rv.seq_stride, rv.head_stride, rv.token_stride, v_last = v.stride()
@@ -624,8 +629,8 @@ class Context:
     def q8_read(self, cache: Q8Cache, pages, start, n: int, count=None, layer: int = 0, n_layers: int | None = None,
                 dtype=None, out_k=None, out_v=None, stream=None):
         """kvmap_q8_read: (k, v) [n_layers][B][H][n][d], the n tokens from start[b] of every sequence, zeros past
-        count[b].  n_layers defaults to the layers from `layer` on; dtype (bf16 by default) to out_k's.  What the call allocates
-        belongs to `stream`."""
+        count[b].  n_layers defaults to the layers from `layer` on; dtype (bf16 by default) to out_k's.
+        What the call allocates belongs to `stream`."""
         torch = _torch()
         L = cache.L - layer if n_layers is None else n_layers
         if dtype is None:
@@ -661,8 +666,8 @@ class Context:
             out = _made_on(stream, lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
         elif out.shape != shape or out.dtype is not q.dtype:
             raise ValueError("out must match q's shape and dtype")
-        if not (q.is_cuda and out.is_cuda):
-            raise ValueError("q and out must be device tensors")
+        if not self.device == cache.index == q.get_device() == out.get_device():
+            raise ValueError("the cache, q and out must be on the context's device")
         rq, ro = self._rows
         rq.layer_stride = ro.layer_stride = 0
         rq.seq_stride, rq.token_stride, rq.head_stride, q_last = q.stride()
@@ -676,7 +681,7 @@ class Context:
                 lse = _made_on(stream, lambda: q.new_empty((B, n_q, H_q), dtype=torch.float32))
             elif lse.shape != (B, n_q, H_q) or lse.dtype != torch.float32:
                 raise ValueError("lse must be float32 [B][n_q][H_q]")
-            lse_ptr = _dev_ptr(lse, "lse")
+            lse_ptr = self._own_ptr(lse, "lse")
         return B, n_q, H_q, out, lse, lse_ptr
 
     def q8_attend(self, cache: Q8Cache, q, pages, lens, max_len: int, layer: int = 0, scale: float | None = None,
@@ -709,7 +714,7 @@ class Context:
             raise ValueError(f"out must be float32 [{n_pos}][{d // 2}][2]")
         keep = []
         rope = _rope(theta, pos0, style, inv_freq, keep)
-        _check(lib().kvmap_rope_table(self._h, ctypes.byref(rope), n_pos, d, _dev_ptr(out, "out"),
+        _check(lib().kvmap_rope_table(self._h, ctypes.byref(rope), n_pos, d, self._own_ptr(out, "out"),
                                       _stream_handle(stream, out.device)), "kvmap_rope_table")
         return out
 
@@ -726,14 +731,12 @@ class Context:
         shape = rope.shape
         if len(shape) != 3 or shape[1] != cache.d // 2 or shape[2] != 2 or rope.dtype is not _torch_module.float32:
             raise ValueError(f"rope must be float32 [positions][{cache.d // 2}][2]")
-        self._rot.table, self._rot.n_pos = _dev_ptr(rope, "rope"), shape[0]
+        self._rot.table, self._rot.n_pos = self._own_ptr(rope, "rope"), shape[0]
         return self._rot_ref
 
     def _paged_rows(self, call, cache, k, v, pages, start, n, count, layer, rope, stream):
         if k.dtype is not cache.dtype or v.dtype is not cache.dtype:
             raise TypeError(f"k and v must be of the cache's dtype, {cache.dtype}")
-        if not self.device == cache.index == k.get_device() == v.get_device():
-            raise ValueError("the cache, k and v must be on the context's device")
         L = self._rows_args(cache, k, v, pages, start, n, count)
         st = call(self._h, cache.ref, layer, L, self._seqs_ref, n, self._rows_ref[0], self._rows_ref[1],
                   self._rotation(rope, cache), _stream_of(stream, cache.index))
@@ -757,8 +760,8 @@ class Context:
                    rope=None, out_k=None, out_v=None, stream=None):
         """kvmap_paged_read: (k, v) [n_layers][B][H][n][d], the n tokens from start[b] of every sequence, zeros past count[b];
         with a table (rope_table) the keys stripped of their rotation (one that scales by s, too, takes a table of cosines and
-        sines over s * s for that).  n_layers defaults to the layers from `layer`
-        on.  What the call allocates belongs to `stream`."""
+        sines over s * s for that).  n_layers defaults to the layers from `layer` on.  What the call
+        allocates belongs to `stream`."""
         torch = _torch()
         L = cache.L - layer if n_layers is None else n_layers
         if out_k is None:
@@ -788,8 +791,6 @@ class Context:
         (out, lse) where lse is a float32 [B][n_q][H_q] tensor or True.  What the call allocates belongs to `stream`."""
         if q.dtype is not cache.dtype:
             raise TypeError(f"q must be of the cache's dtype, {cache.dtype}")
-        if not self.device == cache.index == q.get_device():
-            raise ValueError("the cache and q must be on the context's device")
         B, n_q, H_q, out, lse, lse_ptr = self._attend_args(cache, q, out, lse, stream)
         max_pages = pages.shape[-1]
         st = lib().kvmap_paged_attend(self._h, cache.ref, layer, B, n_q, H_q, self._rows_ref[0],
