@@ -606,6 +606,15 @@ class Context:
         seqs.count = None if count is None else self._q8_ints(count, "count", (B,))
         return L
 
+    @staticmethod
+    def _read_layers(cache, layer, n_layers, out_k, out_v):
+        """How many layers a read gives: n_layers, or without it those of the rows that are given, or all from `layer` on."""
+        given = out_k if out_k is not None else out_v
+        L = n_layers if n_layers is not None else given.shape[0] if given is not None else cache.L - layer
+        if given is not None and given.shape[0] != L:
+            raise ValueError(f"out_k and out_v must have n_layers = {L} layers")
+        return L
+
     def _q8_rows(self, call, cache, k, v, pages, start, n, count, layer, dtype, stream):
         L = self._rows_args(cache, k, v, pages, start, n, count)
         st = call(self._h, cache.ref, layer, L, self._seqs_ref, n, dtype, self._rows_ref[0], self._rows_ref[1],
@@ -629,10 +638,10 @@ class Context:
     def q8_read(self, cache: Q8Cache, pages, start, n: int, count=None, layer: int = 0, n_layers: int | None = None,
                 dtype=None, out_k=None, out_v=None, stream=None):
         """kvmap_q8_read: (k, v) [n_layers][B][H][n][d], the n tokens from start[b] of every sequence, zeros past
-        count[b].  n_layers defaults to the layers from `layer` on; dtype (bf16 by default) to out_k's.
+        count[b].  n_layers defaults to the layers of out_k or out_v, or those from `layer` on; dtype (bf16 by default) to out_k's.
         What the call allocates belongs to `stream`."""
         torch = _torch()
-        L = cache.L - layer if n_layers is None else n_layers
+        L = self._read_layers(cache, layer, n_layers, out_k, out_v)
         if dtype is None:
             dtype = out_k.dtype if out_k is not None else torch.bfloat16
         shape = (L, pages.shape[0], cache.H, n, cache.d)
@@ -760,10 +769,10 @@ class Context:
                    rope=None, out_k=None, out_v=None, stream=None):
         """kvmap_paged_read: (k, v) [n_layers][B][H][n][d], the n tokens from start[b] of every sequence, zeros past count[b];
         with a table (rope_table) the keys stripped of their rotation (one that scales by s, too, takes a table of cosines and
-        sines over s * s for that).  n_layers defaults to the layers from `layer` on.  What the call
+        sines over s * s for that).  n_layers defaults to the layers of out_k or out_v, or those from `layer` on.  What the call
         allocates belongs to `stream`."""
         torch = _torch()
-        L = cache.L - layer if n_layers is None else n_layers
+        L = self._read_layers(cache, layer, n_layers, out_k, out_v)
         if out_k is None:
             out_k = _made_on(stream, lambda: torch.empty((L, pages.shape[0], cache.H, n, cache.d), dtype=cache.dtype,
                                                          device=cache.k.device))

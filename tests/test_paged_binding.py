@@ -120,3 +120,22 @@ def test_tables_lie_on_the_contexts_device(ctx):
     for where in (1, -1):
         with pytest.raises(ValueError):
             ctx.rope_table(80, 64, theta=1e4, out=Tensor(80, 32, 2, dtype=torch.float32, device=where))
+
+
+@pytest.mark.parametrize("kind", ["paged", "q8"])
+def test_a_reads_layers(ctx, kind):
+    """n_layers and the rows that are given have to agree; either says how many."""
+    read = ctx.paged_read if kind == "paged" else ctx.q8_read
+    rows = lambda L: Tensor(L, 4, 2, 7, 64)
+
+    def call(**a):
+        read(_cache(), _ints(4, 5), _ints(4), 7, **a)
+
+    with pytest.raises(Refused):
+        call(out_k=rows(2), out_v=rows(2), n_layers=2)
+    with pytest.raises(Refused):
+        call(out_k=rows(2), out_v=rows(2))
+    for bad in (dict(n_layers=1, out_k=rows(2), out_v=rows(2)), dict(n_layers=2, out_k=rows(1), out_v=rows(1)),
+                dict(n_layers=1, out_k=rows(2), out_v=rows(1)), dict(n_layers=2, out_k=rows(2), out_v=rows(1))):
+        with pytest.raises(ValueError):
+            call(**bad)
