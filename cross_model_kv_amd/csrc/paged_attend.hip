@@ -48,27 +48,23 @@ constexpr int kTile = 32;  // tokens of a wave's step
 __device__ __forceinline__ uint32_t upper_halves(float x0, float x1) {
     return __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
 }
-// What x >= 0 has beyond its upper 16 bits: not negative, and not zero where x is not (at least 2^-126 of it).
-__device__ __forceinline__ float beyond_half(float x) {
-    return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u), fminf(x, 0x1p-126f));
-}
+// What x has beyond its upper 16 bits, of x's sign.
+__device__ __forceinline__ float beyond_half(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
 
-// A turned query's 8 elements as three parts of 8 bits, each cut off, so that they hold all 24 bits (and 2^-125 more at most), all have
-// the element's sign, and none is zero where the element is not: then a key's infinity times the element is the same one in
-// every part's product, and the score has it.
+// A turned query's 8 elements as three parts of 8 bits, each cut off, so that all have the element's sign, and raised by 2^-30 and 2^-40
+// of it, so that none is zero where the element is not (from 2^-86 on): then a key's infinity times the element is the same one
+// in every part's product, and the score has it.
 struct SplitQuery {
     u32x4_t p[3];
     __device__ __forceinline__ void set(const float* x) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float r0 = fabsf(x[2 * i]), r1 = fabsf(x[2 * i + 1]);
-            const uint32_t signs = upper_halves(x[2 * i], x[2 * i + 1]) & 0x80008000u;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                p[k][i] = upper_halves(r0, r1) | signs;
-                r0 = beyond_half(r0);
-                r1 = beyond_half(r1);
-            }
+            const float x0 = x[2 * i], x1 = x[2 * i + 1];
+            const float y0 = fmaf(x0, 0x1p-30f, beyond_half(x0)), y1 = fmaf(x1, 0x1p-30f, beyond_half(x1));
+            const float z0 = fmaf(x0, 0x1p-40f, beyond_half(y0)), z1 = fmaf(x1, 0x1p-40f, beyond_half(y1));
+            p[0][i] = upper_halves(x0, x1);
+            p[1][i] = upper_halves(y0, y1);
+            p[2][i] = upper_halves(z0, z1);
         }
     }
 };
@@ -242,8 +238,8 @@ struct Keys<false, D> {
 // difference to a larger m.  A score is never more than kSlack over its m, and the largest m at most 1 over lse, in base 2: weights of
 // 2^-110 of the row's sum and more stay.)
 // (Two parts, 16 bits: where a row's values nearly cancel, outputs were up to 490 steps of bf16 off, for 21 now and 102 of the
-// formula in 32-bit torch calls, on 64 sequences of up to 16,384 tokens.  The third costs nothing on long sequences and 2 to 4 % on
-// short ones: 4 drafted tokens of 64 sequences of up to 900, 37.4 us for 38.8.)
+// formula in 32-bit torch calls, on 64 sequences of up to 16,384 tokens.  The third is 1 to 3 % of the time of 1 to 4 tokens, 4 drafted ones of
+// 64 sequences of up to 900 in 37.2 us for 36.0, and 6 to 9 % of 16, of 16 sequences of up to 8,192 in 173 for 161.)
 struct SplitWeights {
     bf16x8_t p[3];
     __device__ __forceinline__ void set(const float* x) {
@@ -251,11 +247,13 @@ struct SplitWeights {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float r0 = x[2 * i], r1 = x[2 * i + 1];
+            const float least0 = fminf(r0, 0x1p-126f), least1 = fminf(r1, 0x1p-126f);
+            w[0][i] = upper_halves(r0, r1);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
+            for (int k = 1; k < 3; ++k) {
+                r0 = fmaxf(beyond_half(r0), least0);
+                r1 = fmaxf(beyond_half(r1), least1);
                 w[k][i] = upper_halves(r0, r1);
-                r0 = beyond_half(r0);
-                r1 = beyond_half(r1);
             }
         }
 #pragma unroll

@@ -646,9 +646,10 @@ int kvmap_paged_dropped(kvmap_ctx* ctx, uint32_t* n, void* stream);
  * no token (len[b] = 0, or row i < n_q - len[b]) gives out = 0 and lse = -infinity.  Tokens that a row does not see do not
  * touch it, whatever they hold; infinities and NaN in those that it sees reach it as the formula has it, with `rot` too: an
  * infinite key element gives a score of the sign that it has times the query's, one of -infinity has no weight, and one of
- * +infinity or NaN makes the row and its lse NaN.  (Weights are fp32 numbers: where an infinite value's is below 2^-110 of the
- * row's sum, its score 76 and more under lse, NaN may come in its place.  Sums of weights of up to 2^14 times values are formed in
- * fp32 before they are divided: finite values from 2^114 / len[b] on may give an infinity.)
+ * +infinity or NaN makes the row and its lse NaN, as a query that is not finite may where it is rotated.  (Weights are
+ * fp32 numbers: where an infinite value's is below 2^-110 of the row's sum, its score 76 and more under lse, NaN may come
+ * in its place.  Sums of weights of up to 2^14 times values are formed in fp32 before they are divided: finite values
+ * from 2^114 / len[b] on may give an infinity.)
  * q, out, pages, max_pages, len, max_len, lse, and what is out of range: as in kvmap_q8_attend, with rows of the cache's dtype.
  * bf16: products on the matrix cores with bf16 operands, softmax weights and queries that were rotated with 24 bits.  fp32:
  * products of fp32 operands.  Products' sums and statistics in fp32, the sum of a row's weights in fp64.

@@ -40,8 +40,9 @@ def _run(ctx, k, v, q, pages, lens, dtype, d, rope, cut, scale=None):
     out, lse = ctx.paged_attend(K.PagedCache(kt, vt), qt, _ints(pages), _ints(lens), max_len, rope=rot, lse=True, scale=scale)
     torch.cuda.synchronize()
     scale = d ** -0.5 if scale is None else scale
-    ref = O.attend(dict(k=k64, v=v64), q64, pages, lens, scale, rot=r64)
-    tame = O.attend(dict(k=np.where(np.isfinite(k64), k64, 0), v=v64), q64, pages, lens, scale, rot=r64)
+    with np.errstate(invalid="ignore"):
+        ref = O.attend(dict(k=k64, v=v64), q64, pages, lens, scale, rot=r64)
+        tame = O.attend(dict(k=np.where(np.isfinite(k64), k64, 0), v=v64), q64, pages, lens, scale, rot=r64)
     return _f64(out), _f64(lse), ref, tame
 
 
@@ -127,3 +128,26 @@ def test_an_infinity_far_below_the_largest_score(ctx, dtype, rope, order):
             assert (out[..., 7] == np.inf).all() and (out[..., 9] == -np.inf).all()
         else:
             assert not np.isfinite(out[..., [7, 9]]).any() and not (out[..., 7] == -np.inf).any() and not (out[..., 9] == np.inf).any()
+
+
+@pytest.mark.parametrize("rope", [False, True], ids=["plain", "turned"])
+@pytest.mark.parametrize("n_q,G", [(1, 3), (4, 6), (16, 3)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_queries(ctx, dtype, d, n_q, G, rope):
+    """A query with an element that is not finite: its row is the formula's, or NaN where it is turned, and no other row is touched."""
+    lens, H, page = [40, 300, 17], 2, 16
+    rng = np.random.default_rng([4, d, n_q, G])
+    k, v, pages, _ = _case(rng, lens, H, d, page)
+    q = 1.5 * rng.standard_normal((len(lens), n_q, H * G, d))
+    for b in range(len(lens)):
+        q[b, n_q // 2, b, rng.integers(d)] = ODD[b]
+    out, lse, ref, _ = _run(ctx, k, v, q, pages, lens, dtype, d, rope, False)
+    tame = _run(ctx, k, v, np.where(np.isfinite(q), q, 0), pages, lens, dtype, d, rope, False)[2]
+    r_out, r_lse = ref[0].copy(), ref[1].copy()
+    if rope:
+        for b in range(len(lens)):
+            lost = np.isnan(out[b, n_q // 2, b]).any()
+            assert lost == np.isnan(lse[b, n_q // 2, b])
+            if lost:
+                r_out[b, n_q // 2, b] = r_lse[b, n_q // 2, b] = np.nan
+    _attend_close(out, lse, (r_out, r_lse, ref[2], tame[3]), dtype, d, lens, rope)
