@@ -390,23 +390,6 @@ __device__ __forceinline__ uint32_t steps_upto(const Q8Attend& a, int b0, int st
     return wave_scan(b0 + lane < a.B ? (uint32_t)steps_of(a.len[b0 + lane], a.max_len, step) : 0u);
 }
 
-// One row and 4 dims of a workgroup's waves' sums, joined.
-template <int W, int ROWS, int LDO>
-__device__ __forceinline__ void join_own(const float (*o)[ROWS][LDO], const float (*ml)[ROWS][2], int row, int d4, float& top,
-                                         float& lsum, f32x4_t& sum) {
-    top = ml[0][row][0];
-#pragma unroll
-    for (int w = 1; w < W; ++w) top = fmaxf(top, ml[w][row][0]);
-    sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    lsum = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        const float f = __builtin_amdgcn_exp2f(ml[w][row][0] - top);
-        sum += f * *(const f32x4_t*)&o[w][row][d4];
-        lsum = fmaf(f, ml[w][row][1], lsum);
-    }
-}
-
 template <bool BF16, int D, int NT, bool TURN, bool STREAM>
 __global__ __launch_bounds__(64 * kGroup, (per_simd(BF16, D, NT))) void paged_decode_kernel(Q8Attend a, Rotation rot, Q8Pieces sp) {
     constexpr int W = kGroup, ROWS = 16 * NT, ES = BF16 ? 2 : 4, LDO = D + 4, THREADS = 64 * W, STEP = kTile * W;
@@ -720,7 +703,7 @@ __global__ __launch_bounds__(64 * kGroup, (per_simd(BF16, D, NT))) void paged_de
             const int row = x / (D / 4), d4 = x % (D / 4) * 4;
             float top, lsum;
             f32x4_t sum;
-            join_own<W, ROWS, LDO>(s_o, s_ml, row, d4, top, lsum, sum);
+            join_waves<W, ROWS, LDO>(s_o, s_ml, row, d4, top, lsum, sum);
             if (part) {
                 *(f32x4_t*)(sp.part_o + (slot + row) * D + d4) = sum;
                 if (d4 == 0) *(float2*)(sp.part_ml + (slot + row) * 2) = make_float2(top, lsum);

@@ -67,23 +67,6 @@ __host__ __device__ constexpr int per_cu(bool bf16, int nt) { return bf16 ? (nt 
 template <bool BF16, int NT>
 constexpr bool kThird = per_cu(BF16, NT) == 3;
 
-// One row and 4 dims of the waves' sums, joined.
-template <int ROWS, int LDO>
-__device__ __forceinline__ void join_waves(const float (&s_o)[kWaves][ROWS][LDO], const float (&s_ml)[kWaves][ROWS][2], int row, int d4,
-                                           float& top, float& lsum, f32x4_t& sum) {
-    top = s_ml[0][row][0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, s_ml[w][row][0]);
-    sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    lsum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(s_ml[w][row][0] - top);
-        sum += f * *(const f32x4_t*)&s_o[w][row][d4];
-        lsum = fmaf(f, s_ml[w][row][1], lsum);
-    }
-}
-
 // Steps of one item of each of 64 sequences, summed up to and including the lane's (at most 64 * 2^22).
 __device__ __forceinline__ uint32_t steps_upto(const Q8Attend& a, int b0, int end, int lane) {
     return wave_scan(b0 + lane < end ? (uint32_t)q8_steps(a.len[b0 + lane], a.max_len) : 0u);
@@ -393,7 +376,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
                 const int row = x / (D / 4), d4 = x % (D / 4) * 4;
                 float top, lsum;
                 f32x4_t sum;
-                join_waves<ROWS, LDO>(s_o, s_ml, row, d4, top, lsum, sum);
+                join_waves<kWaves, ROWS, LDO>(s_o, s_ml, row, d4, top, lsum, sum);
                 *(f32x4_t*)(sp.part_o + (slot + row) * D + d4) = sum;
                 if (d4 == 0) *(float2*)(sp.part_ml + (slot + row) * 2) = make_float2(top, lsum);
             }
@@ -402,7 +385,7 @@ __global__ __launch_bounds__(256, (kOccupancy<BF16, D, NT>)) void q8_decode_kern
                 const int row = x / (D / 4), d4 = x % (D / 4) * 4;
                 float top, lsum;
                 f32x4_t sum;
-                join_waves<ROWS, LDO>(s_o, s_ml, row, d4, top, lsum, sum);
+                join_waves<kWaves, ROWS, LDO>(s_o, s_ml, row, d4, top, lsum, sum);
                 if (bad) lsum = nan32();
                 const int i = q8_query(a, row);
                 q8_store_row<BF16>(a, b, i, h * G + row - i * G, d4, top, lsum, sum);

@@ -1,5 +1,5 @@
-// What the kernels that attend over the 8-bit cache share: e4m3 codes, queries and softmax weights as matrix
-// operands, and the constants of the running softmax.
+// What the kernels that attend over the paged caches share: e4m3 codes, queries and softmax weights as matrix
+// operands, the constants of the running softmax, and the joining of its sums.
 #pragma once
 
 #include "common.h"
@@ -229,6 +229,23 @@ __device__ __forceinline__ int settle_sum(double l, float& m, float& lf) {
     lf = (float)__builtin_amdgcn_frexp_mant(l);
     m += (float)e;
     return -e;
+}
+
+// One row and 4 dims of a workgroup's waves' sums, joined.
+template <int W, int ROWS, int LDO>
+__device__ __forceinline__ void join_waves(const float (*o)[ROWS][LDO], const float (*ml)[ROWS][2], int row, int d4, float& top,
+                                           float& lsum, f32x4_t& sum) {
+    top = ml[0][row][0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = fmaxf(top, ml[w][row][0]);
+    sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    lsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml[w][row][0] - top);
+        sum += f * *(const f32x4_t*)&o[w][row][d4];
+        lsum = fmaf(f, ml[w][row][1], lsum);
+    }
 }
 
 // The query of a row.
