@@ -18,16 +18,16 @@
 // a time and need none.  No shared memory and no barrier in the loop but for the low parts of turned queries.
 //
 // bf16 calls: weights as three bf16 parts (24 bits and the exponents of fp32, which they come in), queries that were turned as
-// three too (what their turn in fp32 has).  fp32 calls: products of fp32
-// operands.  Sums and statistics in fp32, a row's sum of weights in fp64.
+// three too (what their turn in fp32 has).  fp32 calls: products of fp32 operands.  Sums and statistics in fp32, a row's sum of
+// weights in fp64.
 //
 // What bounds it: bytes, where there are enough of them.  Keys and values are read once, past the caches and by whole lines of
-// 128 bytes, a tile's 16 KB at a time by each of 8 waves a CU: 64 sequences of 8,192 tokens, 8 KV heads, 2.15 GB in 339 us, 6.35 TB/s
-// (loads alone in the same pattern 6.8; through the caches 5.3), of up to 16,384 in 331, one of 32,768 134 MB in 27 and 4 to
-// join (loads alone 23).  Asking for a tile's keys and values while the one before is multiplied was slower, 61 us for 56 on
-// 8 sequences of 8,192.  Below some thousand tokens a sequence it is the way through one step: lengths, pages, keys, the tile's
-// products and the joining of the waves one after the other, 7.2 us for 130 tokens.  Pieces are joined by a second kernel: by the last
-// piece to come, through memory past the caches, it took 58 us for 38 on one sequence of 32,768 tokens and 63 for 61 on 8 of 8,192.
+// 128 bytes (but fp32 keys), a tile's 16 KB at a time by each of 8 waves a CU: 64 sequences of 8,192 tokens, 8 KV heads, 2.15 GB in
+// 338 to 347 us by card, 6.2 to 6.35 TB/s (loads alone in the same pattern 6.8), one of 32,768 134 MB in 27 and 4 to join.  Asking
+// for a tile's keys and values while the one before is multiplied was slower, 61 us for 56 on 8 sequences of 8,192.  Below some
+// thousand tokens a sequence it is the way through one step: lengths, pages, keys, the tile's products and the joining of the waves
+// one after the other, 7.4 us for 130 tokens.  Pieces are joined by a second kernel: by the last piece to come, through memory past
+// the caches, it took 58 us for 38 on one sequence of 32,768 tokens and 63 for 61 on 8 of 8,192.
 
 #include <algorithm>
 #include <type_traits>
@@ -214,7 +214,8 @@ struct Keys<true, D> {
     }
 };
 
-// fp32: half a line of 16 tokens a load, as the product wants them.
+// fp32: half a line of 16 tokens a load, as the product wants them, and through the caches, where the next load finds the other half (past
+// them 64 sequences of 8,192 tokens take 730 us for 676, 8 of 8,192 104 for 108, 4 of up to 7,091 19.1 for 19.9).
 template <int D>
 struct Keys<false, D> {
     static constexpr int STEPS = D / 16;
@@ -375,14 +376,16 @@ __device__ __forceinline__ T uniform(const T* p) {
     return *(constant_ptr)(uintptr_t)p;
 }
 
-// Waves that a SIMD holds at once, as the registers allow; bf16 rows of 128 dims would fit three times in 16-row tiles, but steps divide
-// better by two, and two have enough in flight (64 sequences of 8,192 tokens 345 us, three 366).
+// Waves that a SIMD holds at once, as the registers allow.  bf16 rows of 128 dims in one 16-row tile, and of 64 dims in two, would fit three
+// times, but steps divide better by two, and two have enough in flight.  The first: 64 sequences of 8,192 tokens 347 us, three 367, one of
+// 32,768 30.6 and 34.5.  The second, 4 drafted tokens, 8 heads, G 8: 8 sequences of 8,192 36 us, three 42, one of 32,768 22 and 28, 16 of
+// up to 16,384 67 and 72 (but 16 of up to 5,003 with 4 heads 25.0 and 24.1, 32 of up to 3,000 27.9 and 25.7).  fp32 spills three times.
 __host__ __device__ constexpr int per_simd(bool bf16, int d, int nt) {
     if (d == 64) return nt == 2 ? 2 : 4;
     return nt == 2 && !bf16 ? 1 : 2;
 }
-// Waves of a workgroup.  (8 in one workgroup a CU, with two row tiles: 22.3 us for 23.4 on 4 drafted tokens of 16 sequences of up to 5,003, 4
-// heads of 64 dims, but 26.5 for 20.5 on 9 of 20 of up to 900, and 161 for 132 on 16 of 16 of up to 8,192, 8 heads of 128 dims, G 8.)
+// Waves of a workgroup.  (8 in one workgroup a CU: 24.1 us for 25.0 on 4 drafted tokens of 16 sequences of up to 5,003, 4 heads of 64 dims, but
+// 29 for 22 on 9 of 20 of up to 900, 207 for 173 on 16 of 16 of up to 8,192, 8 heads of 128 dims, G 8, and 12.5 for 11.4 on one of 4,096.)
 constexpr int kGroup = 4;
 
 // Steps of one item of each of 64 sequences, summed up to and including the lane's.
