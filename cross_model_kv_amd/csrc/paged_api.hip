@@ -176,7 +176,9 @@ extern "C" int kvmap_validate_paged_attend(const kvmap_paged_cache* c, int32_t l
         return report(KVMAP_ERR_SHAPE, "max_len %d exceeds max_pages * page = %d", (int)max_len, (int)(max_pages * c->page));
     if (!len) return report(KVMAP_ERR_INVALID_ARGUMENT, "len is NULL");
     if ((uintptr_t)len & 3) return report(KVMAP_ERR_INVALID_ARGUMENT, "len must be 4-byte aligned");
-    if (!std::isfinite((float)scale) || !(scale > 0)) return report(KVMAP_ERR_INVALID_ARGUMENT, "scale must be finite and > 0");
+    // (the kernels work in base 2, with scale * log2 e)
+    if (!std::isfinite((float)scale * 1.4426950408889634f) || !(scale > 0))
+        return report(KVMAP_ERR_INVALID_ARGUMENT, "scale must be finite, log2 e times it too, and > 0");
     if ((uintptr_t)lse & 3) return report(KVMAP_ERR_INVALID_ARGUMENT, "lse must be 4-byte aligned");
     Range rr, rq, ro, r[2];
     st = check_rotation(rot, c->head_dim, &rr);

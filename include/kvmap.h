@@ -657,7 +657,8 @@ int kvmap_paged_dropped(kvmap_ctx* ctx, uint32_t* n, void* stream);
  * rounding may differ between calls with different company.)  Asynchronous on `stream`.  Long caches are split over
  * workgroups whose results are joined through the context's scratch, as in kvmap_q8_attend and shared with it: calls that may
  * run at the same time, two graphs' replays among them, need a context each.  A call that would have to allocate it while
- * `stream` is being captured is refused (INVALID_ARGUMENT): kvmap_paged_reserve.  Errors as kvmap_paged_append; SHAPE also for
+ * `stream` is being captured is refused (INVALID_ARGUMENT): kvmap_paged_reserve.  Errors as kvmap_paged_append;
+ * INVALID_ARGUMENT also for a scale that is not > 0 or whose product with log2 e is no finite fp32 number; SHAPE also for
  * B * H_kv >= 2^16, H_q > 2^16, B * n_q * H_q >= 2^24, max_len >= 2^30 and a table shorter than max_len; UNSUPPORTED also for
  * n_q > 16. */
 int kvmap_paged_attend(kvmap_ctx* ctx, const kvmap_paged_cache* cache, int32_t layer, int32_t B, int32_t n_q, int32_t H_q,
