@@ -619,6 +619,8 @@ int kvmap_rope_table(kvmap_ctx* ctx, const kvmap_rope* rope, int64_t n_pos, int3
  * rows (layer - layer0, b, head, i), i < count[b].  With `rot` (NULL: keys enter as they are) pair (x, y) = (i, i + d/2)
  * of the key at position p enters as (x cos - y sin, y cos + x sin) with row p of the table, formed in fp32 and rounded
  * once.  Everything else in the pages is left as it is; appending the same tokens again changes nothing.
+ * Two tokens of one call that enter the same row (pages that sequences share, or that one lists twice) leave either's
+ * elements there, in no order.
  * A token whose position or page is out of range (start < 0, count outside 0 .. n, beyond max_pages, a page outside
  * 0 .. n_pages - 1, a position not in the table) is not written, and counted: see kvmap_paged_dropped.
  * Asynchronous on `stream`, allocates nothing, may be captured into a graph.
