@@ -8,7 +8,7 @@ import numpy as np
 
 
 def table(n_pos, d, theta=None, inv_freq=None, pos0=0):
-    """Cosines and sines in float64, from angles reduced in integer turns of a longer product."""
+    """Cosines and sines in float64 of the angles position times frequency, rounded once each."""
     f = theta ** (-2.0 * np.arange(d // 2) / d) if inv_freq is None else np.asarray(inv_freq, np.float64)
     a = np.arange(pos0, pos0 + n_pos, dtype=np.float64)[:, None] * f
     return np.stack([np.cos(a), np.sin(a)], -1)
